@@ -28,7 +28,7 @@ EXPORTS = ["dg_create", "dg_destroy", "dg_prefill", "dg_denoise_step", "dg_denoi
            "dg_debug_sample", "dg_debug_entropy_sample", "dg_debug_entropy", "dg_debug_wait_timeout",
            "dg_debug_gemm", "dg_debug_profile",
            "dg_debug_profile_read", "dg_debug_launch_count", "dg_debug_timeline_reset", "dg_debug_timeline",
-           "dg_lmhead_argmax_static"]
+           "dg_lmhead_argmax_static", "dg_paged_plan", "dg_paged_append", "dg_paged_attention"]
 
 # kernel ids of the timeline records (DG_K_* in dg.h)
 TIMELINE_KERNELS = {10: "gemm_dense", 11: "gemm_moe", 13: "gemm_lmhead", 20: "attention", 21: "attn_merge", 30: "route_dispatch",
@@ -73,6 +73,15 @@ class dg_timeline_record(ctypes.Structure):
 
 class dg_entropy_args(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("gamma", ctypes.c_float), ("stop_entropy", ctypes.c_float)]
+
+
+class dg_paged_attention_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k_pages", "v_pages", "block_table", "kv_lens", "cu_rows", "out",
+                                               "lse")] + \
+               [(n, ctypes.c_int64) for n in ("q_stride", "table_stride")] + \
+               [(n, ctypes.c_int32) for n in ("n_rows", "batch", "n_q_heads", "n_kv_heads", "head_dim", "n_pages",
+                                              "page_size", "table_width", "causal", "max_rows")] + \
+               [("scale", ctypes.c_float)]
 
 
 class DGError(RuntimeError):
@@ -123,6 +132,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dg_debug_timeline_reset": ([P], I32),
         "dg_debug_timeline": ([P, P, I32, ctypes.POINTER(I64)], I32),
         "dg_lmhead_argmax_static": ([P, I32, I32, P, I32, F32, P, P, P, P], I32),
+        "dg_paged_plan": ([P, P, I32, P, I32, I64, P, I32, P, I32, P, P, P, P, I32, P, P], I32),
+        "dg_paged_append": ([P, I64, I32, I32, I32, I32, P, P, P, I32, P, P, I32, I32, P, P], I32),
+        "dg_paged_attention": ([ctypes.POINTER(dg_paged_attention_args), P], I32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -458,6 +470,157 @@ def lmhead_argmax_static(z, embed, temperature, argmax=None, lse=None, conf=None
             return 1
     return lib.dg_lmhead_argmax_static(_ptr(z), n_rows, d, _ptr(embed), embed.shape[0], float(temperature),
                                        _ptr(argmax), _ptr(lse), _ptr(conf), stream)
+
+
+# --- paged KV cache ---
+# Context-free calls on torch CUDA tensors.  They run on torch's current stream
+# of the tensors' device, allocate nothing and synchronise nothing; arguments
+# are checked first, and a bad one raises DGError with nothing launched.
+
+def _paged_dev(t, dtype, ndim, what, dev=None):
+    """t as an operand: a CUDA tensor of `dtype` with `ndim` dimensions, the
+    last one dense, on `dev` (the first operand's device)."""
+    import torch
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.dim() != ndim:
+        _invalid(f"{what}: expected a {ndim}-dimensional CUDA tensor of {dtype}, got "
+                 f"{getattr(t, 'dtype', type(t).__name__)} {tuple(getattr(t, 'shape', ()))} on "
+                 f"{getattr(t, 'device', '?')}")
+    if dev is not None and t.device != dev:
+        _invalid(f"{what}: on {t.device}, the other tensors are on {dev}")
+    return t
+
+
+def _paged_flat(t, dtype, n, what, dev):
+    _paged_dev(t, dtype, 1, what, dev)
+    if t.numel() < n or not t.is_contiguous():
+        _invalid(f"{what}: {t.numel()} elements{'' if t.is_contiguous() else ' (strided)'}, the call needs {n}")
+    return t.data_ptr()
+
+
+def _paged_pools(k_pages, v_pages, dev):
+    import torch
+    for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _paged_dev(t, torch.bfloat16, 4, what, dev)
+        if not t.is_contiguous():
+            _invalid(f"{what}: strided")
+    if k_pages.shape != v_pages.shape:
+        _invalid(f"k_pages {tuple(k_pages.shape)} and v_pages {tuple(v_pages.shape)} differ")
+    return k_pages.shape                          # n_pages, n_kv_heads, page_size, head_dim
+
+
+def _paged_call(name, dev, *args):
+    """The call on torch's current stream of `dev`, with that device current."""
+    import torch
+    f = getattr(load_library(), name)
+    if torch.cuda.current_device() == dev.index:
+        st = f(*args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = f(*args, torch.cuda.current_stream().cuda_stream)
+    if st != DG_OK:
+        raise DGError(st, f"{name} refused (shape, alignment or capacity; see include/dg.h)")
+
+
+def rope_table(n_positions: int, head_dim: int, base: float = 10000.0, device="cuda"):
+    """(cos, sin) of position * base^(-2j / head_dim), angles in double
+    precision, stored fp32: [n_positions, head_dim / 2, 2], the table a
+    context builds for itself and paged_append reads."""
+    import torch
+    j = torch.arange(head_dim // 2, dtype=torch.float64, device=device)
+    a = torch.arange(n_positions, dtype=torch.float64, device=device)[:, None] * base ** (-2.0 * j / head_dim)
+    return torch.stack([a.cos(), a.sin()], -1).float()
+
+
+def paged_plan(cached_lens, new_rows, block_table, free_pages, free_state, page_size, cu_rows, kv_lens, positions,
+               slots, free_state_out):
+    """dg_paged_plan on torch tensors (all int32): block tables, slots and
+    positions of the new rows from the requests' lengths.  block_table
+    [batch, width] and free_pages [n_pages] are updated in place, cu_rows
+    [batch + 1], kv_lens [batch], positions and slots [row capacity] and
+    free_state_out [4] are written; free_state [>= 2] is read (pass the last
+    call's free_state_out, and another buffer to write)."""
+    import torch
+    i32 = torch.int32
+    dev = _paged_dev(block_table, i32, 2, "block_table").device
+    B, W = block_table.shape
+    if block_table.stride(1) != 1:
+        _invalid("block_table: entries of a row must be adjacent")
+    _paged_dev(free_pages, i32, 1, "free_pages", dev)
+    _paged_dev(slots, i32, 1, "slots", dev)
+    n_pages, cap = free_pages.numel(), slots.numel()
+    _paged_call("dg_paged_plan", dev,
+                _paged_flat(cached_lens, i32, B, "cached_lens", dev), _paged_flat(new_rows, i32, B, "new_rows", dev),
+                B, block_table.data_ptr(), W, block_table.stride(0) if B > 1 else W,
+                _paged_flat(free_pages, i32, 1, "free_pages", dev), n_pages,
+                _paged_flat(free_state, i32, 2, "free_state", dev), int(page_size),
+                _paged_flat(cu_rows, i32, B + 1, "cu_rows", dev), _paged_flat(kv_lens, i32, B, "kv_lens", dev),
+                _paged_flat(positions, i32, cap, "positions", dev), _paged_flat(slots, i32, cap, "slots", dev), cap,
+                _paged_flat(free_state_out, i32, 4, "free_state_out", dev))
+
+
+def paged_append(qkv, positions, slots, rope, k_pages, v_pages, q_out):
+    """dg_paged_append on torch tensors: rotate q and k of the rows qkv
+    [rows, (Hq + 2 Hkv) * D] bf16 at `positions`, write q to q_out
+    [rows, Hq, D], k and v to `slots` of the pages [n_pages, Hkv, page_size,
+    D].  positions and slots (int32) hold at least `rows` entries; rope is
+    rope_table's."""
+    import torch
+    dev = _paged_dev(qkv, torch.bfloat16, 2, "qkv").device
+    rows = qkv.shape[0]
+    n_pages, hkv, page, d = _paged_pools(k_pages, v_pages, dev)
+    _paged_dev(q_out, torch.bfloat16, 3, "q_out", dev)
+    hq = q_out.shape[1]
+    if q_out.shape != (rows, hq, d) or not q_out.is_contiguous():
+        _invalid(f"q_out: expected a contiguous [{rows}, Hq, {d}] tensor, got {tuple(q_out.shape)}")
+    if qkv.shape[1] != (hq + 2 * hkv) * d or (qkv.stride(1) != 1 and rows):
+        _invalid(f"qkv: expected rows of {(hq + 2 * hkv) * d} adjacent elements, got {tuple(qkv.shape)}")
+    _paged_dev(rope, torch.float32, 3, "rope", dev)
+    if rope.shape[1:] != (d // 2, 2) or not rope.is_contiguous():
+        _invalid(f"rope: expected a contiguous [positions, {d // 2}, 2] tensor, got {tuple(rope.shape)}")
+    if rows == 0:
+        return
+    _paged_call("dg_paged_append", dev, qkv.data_ptr(), qkv.stride(0) if rows > 1 else qkv.shape[1], rows, hq, hkv, d,
+                _paged_flat(positions, torch.int32, rows, "positions", dev),
+                _paged_flat(slots, torch.int32, rows, "slots", dev), rope.data_ptr(), rope.shape[0],
+                k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, q_out.data_ptr())
+
+
+def paged_attention(q, k_pages, v_pages, block_table, kv_lens, cu_rows, out, lse=None, causal=False, max_rows=0,
+                    scale=None):
+    """dg_paged_attention on torch tensors: attention of the packed rows q
+    [rows, Hq, D] bf16 over their requests' pages into out [rows, Hq, D] bf16
+    and, where given, lse [rows, Hq] fp32.  block_table [batch, width],
+    kv_lens [batch] and cu_rows [batch + 1] are int32 (paged_plan's).  With
+    causal, row i of a request's n sees the keys before its own and its own,
+    the n new rows being the request's last; else all of them.  max_rows is an
+    upper bound of a request's rows where the caller knows one (it picks the
+    kernel); scale defaults to D ** -0.5."""
+    import torch
+    dev = _paged_dev(q, torch.bfloat16, 3, "q").device
+    rows, hq, d = q.shape
+    n_pages, hkv, page, dk = _paged_pools(k_pages, v_pages, dev)
+    if dk != d or (rows and (q.stride(2) != 1 or q.stride(1) != d)):
+        _invalid(f"q: expected [rows, Hq, {dk}] with adjacent heads, got {tuple(q.shape)}")
+    _paged_dev(out, torch.bfloat16, 3, "out", dev)
+    if out.shape != q.shape or not out.is_contiguous():
+        _invalid(f"out: expected a contiguous {tuple(q.shape)} tensor, got {tuple(out.shape)}")
+    if lse is not None:
+        _paged_dev(lse, torch.float32, 2, "lse", dev)
+        if lse.shape != (rows, hq) or not lse.is_contiguous():
+            _invalid(f"lse: expected a contiguous {(rows, hq)} tensor, got {tuple(lse.shape)}")
+    _paged_dev(block_table, torch.int32, 2, "block_table", dev)
+    B, W = block_table.shape
+    if block_table.stride(1) != 1 and W > 1:
+        _invalid("block_table: entries of a row must be adjacent")
+    if rows == 0 or B == 0:
+        return
+    a = dg_paged_attention_args(
+        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
+        _paged_flat(kv_lens, torch.int32, B, "kv_lens", dev), _paged_flat(cu_rows, torch.int32, B + 1, "cu_rows", dev),
+        out.data_ptr(), None if lse is None else lse.data_ptr(), q.stride(0) if rows > 1 else hq * d,
+        block_table.stride(0) if B > 1 else W, rows, B, hq, hkv, d, n_pages, page, W, 1 if causal else 0,
+        int(max_rows), d ** -0.5 if scale is None else float(scale))
+    _paged_call("dg_paged_attention", dev, ctypes.byref(a))
 
 
 def anneal_temperature(step: int, max_steps: int = 48, t_first: float = 0.8, t_last: float = 0.4) -> float:

@@ -1626,3 +1626,5 @@ extern "C" dg_status dg_lmhead_argmax_static(const void* z, int32_t n_rows, int3
     return DG_ERR_CUDA;
   return DG_OK;
 }
+
+#include "paged_api.cuh"

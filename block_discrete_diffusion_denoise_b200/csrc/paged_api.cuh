@@ -1,0 +1,160 @@
+// C ABI of the paged KV cache (include/dg.h, dg_paged_*): argument checks on
+// the host, launch shapes, and the choice of the attention kernel.  Included
+// by engine.cu, whose tensor-map helpers it uses.
+#pragma once
+
+#include "paged.cuh"
+
+namespace {
+
+// log2 of a supported page size, -1 for any other
+int page_shift_of(int32_t page_size) {
+  switch (page_size) {
+    case 16: return 4;
+    case 32: return 5;
+    case 64: return 6;
+    case 128: return 7;
+    default: return -1;
+  }
+}
+
+// heads the paged kernels serve: the shapes of dg_config
+dg_status check_heads(int Hq, int Hkv, int D) {
+  if (Hq <= 0 || Hkv <= 0 || D <= 0) return DG_ERR_INVALID_ARG;
+  if ((D != 64 && D != 128 && D != 176) || Hq % Hkv || ATC_BQ % (Hq / Hkv) || Hq > 1024) return DG_ERR_UNSUPPORTED;
+  return DG_OK;
+}
+
+// a launch's own status; an error that the caller left pending is neither
+// reported nor cleared
+template <typename P>
+dg_status paged_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
+  cudaLaunchConfig_t lc{};
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = static_cast<cudaStream_t>(stream);
+  return cudaLaunchKernelEx(&lc, kernel, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+dg_status dg_paged_plan(const int32_t* cached, const int32_t* fresh, int32_t batch, int32_t* table, int32_t width,
+                        int64_t table_stride, int32_t* free_pages, int32_t n_pages, const int32_t* free_state,
+                        int32_t page_size, int32_t* cu_rows, int32_t* kv_lens, int32_t* positions, int32_t* slots,
+                        int32_t row_capacity, int32_t* free_state_out, void* cuda_stream) {
+  const int shift = page_shift_of(page_size);
+  if (!cached || !fresh || !table || !free_pages || !free_state || !cu_rows || !kv_lens || !free_state_out ||
+      batch <= 0 || width <= 0 || table_stride < width || n_pages <= 0 || row_capacity < 0 ||
+      (row_capacity > 0 && (!positions || !slots)))
+    return DG_ERR_INVALID_ARG;
+  if (shift < 0) return DG_ERR_UNSUPPORTED;
+  // inputs that other CTAs still read must not be outputs
+  if (free_state == free_state_out || cached == kv_lens || fresh == kv_lens) return DG_ERR_INVALID_ARG;
+  if (n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;  // a slot is 32 bits
+  PagedPlanParams p;
+  p.cached = cached;
+  p.fresh = fresh;
+  p.table = table;
+  p.table_stride = table_stride;
+  p.ring = free_pages;
+  p.state = free_state;
+  p.cu_rows = cu_rows;
+  p.kv_lens = kv_lens;
+  p.positions = positions;
+  p.slots = slots;
+  p.state_out = free_state_out;
+  p.batch = batch;
+  p.width = width;
+  p.n_pages = n_pages;
+  p.page_shift = shift;
+  p.row_cap = row_capacity;
+  // one CTA per request up to a wave of them; strips of a request's rows where
+  // there are few requests of many rows
+  const int gx = std::min(batch, 148);
+  const int64_t strips = row_capacity / (static_cast<int64_t>(batch) * 2 * PLAN_THREADS);
+  const int gy = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(strips, 148 / gx)));
+  return paged_launch(paged_plan_kernel, dim3(gx, gy), PLAN_THREADS, 0, cuda_stream, p);
+}
+
+dg_status dg_paged_append(const void* qkv, int64_t qkv_stride, int32_t n_rows, int32_t n_q_heads, int32_t n_kv_heads,
+                          int32_t head_dim, const int32_t* positions, const int32_t* slots, const float* rope,
+                          int32_t n_positions, void* k_pages, void* v_pages, int32_t n_pages, int32_t page_size,
+                          void* q_out, void* cuda_stream) {
+  if (!qkv || !positions || !slots || !rope || !k_pages || !v_pages || !q_out || n_rows < 0 || n_positions <= 0 ||
+      n_pages <= 0 || !aligned16(qkv) || !aligned16(rope) || !aligned16(k_pages) || !aligned16(v_pages) ||
+      !aligned16(q_out))
+    return DG_ERR_INVALID_ARG;
+  const dg_status hs = check_heads(n_q_heads, n_kv_heads, head_dim);
+  if (hs != DG_OK) return hs;
+  const int shift = page_shift_of(page_size);
+  if (shift < 0) return DG_ERR_UNSUPPORTED;
+  const int heads = n_q_heads + 2 * n_kv_heads;
+  if (qkv_stride < static_cast<int64_t>(heads) * head_dim || qkv_stride % 8) return DG_ERR_INVALID_ARG;
+  if (n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;
+  if (n_rows == 0) return DG_OK;
+  PagedAppendParams p;
+  p.qkv = static_cast<const uint16_t*>(qkv);
+  p.qkv_stride = qkv_stride;
+  p.positions = positions;
+  p.slots = slots;
+  p.rope = reinterpret_cast<const float4*>(rope);
+  p.k = static_cast<uint16_t*>(k_pages);
+  p.v = static_cast<uint16_t*>(v_pages);
+  p.q = static_cast<uint16_t*>(q_out);
+  p.n_slots = static_cast<int64_t>(n_pages) << shift;
+  p.rows = n_rows;
+  p.n_positions = n_positions;
+  p.Hq = n_q_heads;
+  p.Hkv = n_kv_heads;
+  p.page_shift = shift;
+  const int64_t items = static_cast<int64_t>(n_rows) * ((heads + APPEND_HEADS - 1) / APPEND_HEADS) * (head_dim / 16);
+  const int64_t grid = (items + APPEND_THREADS - 1) / APPEND_THREADS;
+  if (grid > INT32_MAX) return DG_ERR_CAPACITY;
+  auto* kern = head_dim == 64 ? paged_append_kernel<64>
+               : head_dim == 128 ? paged_append_kernel<128> : paged_append_kernel<176>;
+  return paged_launch(kern, dim3(static_cast<unsigned>(grid)), APPEND_THREADS, 0, cuda_stream, p);
+}
+
+dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream) {
+  if (!a || !a->q || !a->k_pages || !a->v_pages || !a->block_table || !a->kv_lens || !a->cu_rows || !a->out ||
+      a->n_rows < 0 || a->batch <= 0 || a->n_pages <= 0 || a->table_width <= 0 || a->table_stride < a->table_width ||
+      !(a->scale > 0.f) || !(a->scale < INFINITY) || !aligned16(a->q) || !aligned16(a->k_pages) ||
+      !aligned16(a->v_pages) || !aligned16(a->out))
+    return DG_ERR_INVALID_ARG;
+  const dg_status hs = check_heads(a->n_q_heads, a->n_kv_heads, a->head_dim);
+  if (hs != DG_OK) return hs;
+  const int shift = page_shift_of(a->page_size);
+  if (shift < 0) return DG_ERR_UNSUPPORTED;
+  if (a->q_stride < static_cast<int64_t>(a->n_q_heads) * a->head_dim || a->q_stride % 8) return DG_ERR_INVALID_ARG;
+  if (a->n_pages > (INT32_MAX >> shift) || a->table_width > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;
+  if (a->n_rows == 0) return DG_OK;
+  PagedAttnParams p;
+  p.q = static_cast<const uint16_t*>(a->q);
+  p.q_stride = a->q_stride;
+  p.k = static_cast<const uint16_t*>(a->k_pages);
+  p.v = static_cast<const uint16_t*>(a->v_pages);
+  p.table = a->block_table;
+  p.table_stride = a->table_stride;
+  p.kv_lens = a->kv_lens;
+  p.cu_rows = a->cu_rows;
+  p.o = static_cast<uint16_t*>(a->out);
+  p.lse = a->lse;
+  p.rows = a->n_rows;
+  p.batch = a->batch;
+  p.Hq = a->n_q_heads;
+  p.Hkv = a->n_kv_heads;
+  p.n_pages = a->n_pages;
+  p.page_shift = shift;
+  p.width = a->table_width;
+  p.causal = a->causal != 0;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
+  const int64_t units = static_cast<int64_t>(a->n_rows) * a->n_q_heads;
+  auto* kern = a->head_dim == 64 ? paged_attn_simple_kernel<64>
+               : a->head_dim == 128 ? paged_attn_simple_kernel<128> : paged_attn_simple_kernel<176>;
+  return paged_launch(kern, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0, cuda_stream, p);
+}
+
+}  // extern "C"

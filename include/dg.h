@@ -402,6 +402,121 @@ dg_status dg_lmhead_argmax_static(const void* z_dev, int32_t n_rows, int32_t d_m
                                   int32_t vocab, float temperature, int32_t* argmax_dev, float* lse_dev,
                                   float* conf_dev, void* cuda_stream);
 
+/* ---------------------------------------------------------------------------
+ * Paged KV cache: requests of different lengths over one pool of pages.
+ *
+ * The contiguous cache of a context gives every sequence of a call the same
+ * length.  These calls serve requests of any lengths: their keys and values
+ * lie in pages of one pool, a block table says which, and no context is
+ * needed.
+ *
+ * Layouts
+ *   k_pages, v_pages [n_pages][n_kv_heads][page_size][head_dim] bf16
+ *   block_table      [batch][table_width] int32 page ids, rows table_stride
+ *                    elements apart; request b's position t lies in page
+ *                    block_table[b][t / page_size] at offset t % page_size
+ *   slot             page * page_size + offset (int32)
+ *   rows             the new rows of all requests, packed: request b's are
+ *                    [cu_rows[b], cu_rows[b + 1])
+ * Supported: page_size 16, 32, 64 or 128; head_dim and head counts as in
+ * dg_config; n_pages * page_size below 2^31 (DG_ERR_CAPACITY otherwise).
+ *
+ * Every call is asynchronous on cuda_stream (NULL: the legacy default stream)
+ * of the current device, allocates nothing, may be captured into a CUDA graph,
+ * and reports only its own launches' status.  Lengths and tables are read on
+ * the device, so a captured call may be replayed with others.  Index values
+ * from device memory are checked there: an id or a length that is out of range
+ * is never followed (what it does instead stands at each call).
+ * ------------------------------------------------------------------------- */
+
+/* Block tables, slots and positions of a call's new rows, from the requests'
+ * lengths.  With held = ceil(cached / page_size) and need = ceil((cached +
+ * new) / page_size), request b takes need - held pages from the pool, or gives
+ * held - need back where new_rows is negative (-cached releases it all).
+ *   cached_dev, new_dev [batch] int32
+ *   block_table_dev     entries [held, need) are written, the others left
+ *   free_pages_dev      [n_pages] ring of free page ids; pages are taken from
+ *                       its head and put behind its tail, in the order of
+ *                       request and page
+ *   free_state_dev      [2] int32 {index of the ring's head, free pages}
+ *   cu_rows_dev         [batch + 1] out: exclusive sums of max(new, 0)
+ *   kv_lens_dev         [batch] out: cached + new
+ *   positions_dev, slots_dev [row_capacity] out: cached + i and its slot for
+ *                       row i of each request; entries behind the last row
+ *                       are left as they were (both may be NULL with
+ *                       row_capacity 0)
+ *   free_state_out_dev  [4] int32 out: {head, free pages} after the call,
+ *                       missing pages, reasons
+ * All or nothing: where the free pages do not suffice (missing > 0) or a
+ * reason is set (bit 0: a negative length, or new < -cached; bit 1: a request
+ * needs more than table_width pages; bit 2: more than row_capacity rows; bit
+ * 3: free_state is no state of the ring), no page changes hands, kv_lens
+ * is cached and the rows' slots are -1, which dg_paged_append skips.
+ * free_state_out_dev must not be free_state_dev, nor kv_lens_dev an input. */
+dg_status dg_paged_plan(const int32_t* cached_dev, const int32_t* new_dev, int32_t batch, int32_t* block_table_dev,
+                        int32_t table_width, int64_t table_stride, int32_t* free_pages_dev, int32_t n_pages,
+                        const int32_t* free_state_dev, int32_t page_size, int32_t* cu_rows_dev,
+                        int32_t* kv_lens_dev, int32_t* positions_dev, int32_t* slots_dev, int32_t row_capacity,
+                        int32_t* free_state_out_dev, void* cuda_stream);
+
+/* Rotary positions on the new rows and their way into the pages: rows
+ * qkv_dev [n_rows][(Hq + 2 Hkv) * D] bf16 (query, key, value heads; rows
+ * qkv_stride elements apart, a multiple of 8) are rotated in pairs (j, j + D/2)
+ * by rope_dev [n_positions][D/2][2] fp32 (cos, sin) at positions_dev [n_rows];
+ * q_out_dev [n_rows][Hq][D] bf16 receives q, the pages k and v at slots_dev
+ * [n_rows].  A row whose slot is outside the pool writes no k and v; a row whose
+ * position is outside the table writes none either, and NaN as its q.  The
+ * slots of a call must differ from one another (of two rows with one slot,
+ * which one's values stay is not defined). */
+dg_status dg_paged_append(const void* qkv_dev, int64_t qkv_stride, int32_t n_rows, int32_t n_q_heads,
+                          int32_t n_kv_heads, int32_t head_dim, const int32_t* positions_dev,
+                          const int32_t* slots_dev, const float* rope_dev, int32_t n_positions, void* k_pages_dev,
+                          void* v_pages_dev, int32_t n_pages, int32_t page_size, void* q_out_dev,
+                          void* cuda_stream);
+
+/* Arguments of dg_paged_attention.
+ *   q           [n_rows][Hq][D] bf16, rows q_stride elements apart (a multiple of 8)
+ *   out         [n_rows][Hq][D] bf16
+ *   lse         [n_rows][Hq] fp32 or NULL: log sum exp (natural) of a row's scaled scores
+ *   scale       factor of the scores, usually 1 / sqrt(D)
+ *   causal      0: every row sees all keys of its request; 1: row i of n sees
+ *               keys [0, kv_lens - n + i]
+ *   max_rows    an upper bound of the rows of one request, or 0 (n_rows): it
+ *               picks the kernel, the result does not depend on it */
+typedef struct dg_paged_attention_args {
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  const int32_t* block_table;
+  const int32_t* kv_lens;
+  const int32_t* cu_rows;
+  void* out;
+  float* lse;
+  int64_t q_stride;
+  int64_t table_stride;
+  int32_t n_rows;
+  int32_t batch;
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t table_width;
+  int32_t causal;
+  int32_t max_rows;
+  float scale;
+} dg_paged_attention_args;
+
+/* Attention of packed rows over their requests' pages (codemajin.net
+ * "DiffusionGemma architecture", section 3.2: a canvas over the cache and
+ * itself, or the causal encoder), for anything from one row per request to
+ * whole prompts.  Rows outside [cu_rows[0], cu_rows[batch]) are left as they
+ * were; cu_rows must not decrease.  Keys beyond table_width pages, and keys of
+ * a page id outside the pool, are masked; a row that sees no key gets zeros
+ * and lse = -inf.  What lies in the pages at masked positions (NaN included)
+ * has no effect. */
+dg_status dg_paged_attention(const dg_paged_attention_args* args, void* cuda_stream);
+
 #ifdef __cplusplus
 }
 #endif
