@@ -28,7 +28,8 @@ EXPORTS = ["dg_create", "dg_destroy", "dg_prefill", "dg_denoise_step", "dg_denoi
            "dg_debug_sample", "dg_debug_entropy_sample", "dg_debug_entropy", "dg_debug_wait_timeout",
            "dg_debug_gemm", "dg_debug_profile",
            "dg_debug_profile_read", "dg_debug_launch_count", "dg_debug_timeline_reset", "dg_debug_timeline",
-           "dg_lmhead_argmax_static", "dg_paged_plan", "dg_paged_append", "dg_paged_attention"]
+           "dg_lmhead_argmax_static", "dg_paged_plan", "dg_paged_append",
+           "dg_paged_attention_workspace", "dg_paged_attention"]
 
 # kernel ids of the timeline records (DG_K_* in dg.h)
 TIMELINE_KERNELS = {10: "gemm_dense", 11: "gemm_moe", 13: "gemm_lmhead", 20: "attention", 21: "attn_merge", 30: "route_dispatch",
@@ -77,8 +78,8 @@ class dg_entropy_args(ctypes.Structure):
 
 class dg_paged_attention_args(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k_pages", "v_pages", "block_table", "kv_lens", "cu_rows", "out",
-                                               "lse")] + \
-               [(n, ctypes.c_int64) for n in ("q_stride", "table_stride")] + \
+                                               "lse", "workspace")] + \
+               [(n, ctypes.c_int64) for n in ("workspace_bytes", "q_stride", "table_stride")] + \
                [(n, ctypes.c_int32) for n in ("n_rows", "batch", "n_q_heads", "n_kv_heads", "head_dim", "n_pages",
                                               "page_size", "table_width", "causal", "max_rows")] + \
                [("scale", ctypes.c_float)]
@@ -134,6 +135,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dg_lmhead_argmax_static": ([P, I32, I32, P, I32, F32, P, P, P, P], I32),
         "dg_paged_plan": ([P, P, I32, P, I32, I64, P, I32, P, I32, P, P, P, P, I32, P, P], I32),
         "dg_paged_append": ([P, I64, I32, I32, I32, I32, P, P, P, I32, P, P, I32, I32, P, P], I32),
+        "dg_paged_attention_workspace": ([ctypes.POINTER(dg_paged_attention_args), ctypes.POINTER(I64)], I32),
         "dg_paged_attention": ([ctypes.POINTER(dg_paged_attention_args), P], I32),
     }
     for name, (args, res) in sig.items():
@@ -508,15 +510,14 @@ def _paged_pools(k_pages, v_pages, dev):
     return k_pages.shape                          # n_pages, n_kv_heads, page_size, head_dim
 
 
-def _paged_call(name, dev, *args):
+def _paged_call(name, dev, *args, stream=True):
     """The call on torch's current stream of `dev`, with that device current."""
     import torch
     f = getattr(load_library(), name)
-    if torch.cuda.current_device() == dev.index:
-        st = f(*args, torch.cuda.current_stream().cuda_stream)
-    else:
+    if torch.cuda.current_device() != dev.index:
         with torch.cuda.device(dev):
-            st = f(*args, torch.cuda.current_stream().cuda_stream)
+            return _paged_call(name, dev, *args, stream=stream)
+    st = f(*args, torch.cuda.current_stream().cuda_stream) if stream else f(*args)
     if st != DG_OK:
         raise DGError(st, f"{name} refused (shape, alignment or capacity; see include/dg.h)")
 
@@ -617,9 +618,14 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_lens, cu_rows, out, lse
     a = dg_paged_attention_args(
         q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
         _paged_flat(kv_lens, torch.int32, B, "kv_lens", dev), _paged_flat(cu_rows, torch.int32, B + 1, "cu_rows", dev),
-        out.data_ptr(), None if lse is None else lse.data_ptr(), q.stride(0) if rows > 1 else hq * d,
+        out.data_ptr(), None if lse is None else lse.data_ptr(), None, 0, q.stride(0) if rows > 1 else hq * d,
         block_table.stride(0) if B > 1 else W, rows, B, hq, hkv, d, n_pages, page, W, 1 if causal else 0,
         int(max_rows), d ** -0.5 if scale is None else float(scale))
+    need = ctypes.c_int64()
+    _paged_call("dg_paged_attention_workspace", dev, ctypes.byref(a), ctypes.byref(need), stream=False)
+    # from torch's allocator: calls on other streams and in other graphs get memory of their own
+    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
+    a.workspace, a.workspace_bytes = ws.data_ptr(), need.value
     _paged_call("dg_paged_attention", dev, ctypes.byref(a))
 
 

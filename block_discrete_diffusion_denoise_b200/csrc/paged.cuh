@@ -256,76 +256,4 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
   }
 }
 
-// ----------------------------------------------------------------------------
-// Attention.  Row i of request b (n rows, kv keys) sees keys [0, kv), or with
-// `causal` [0, kv - n + i + 1): o = softmax(q K^T / sqrt(D)) V over them, and
-// lse = log sum exp of its scores.  Keys of a page id outside the pool count
-// as masked; a row that sees nothing gives zeros and lse = -inf.
-// ----------------------------------------------------------------------------
-struct PagedAttnParams {
-  const uint16_t* q;           // [rows][Hq][D], row stride q_stride
-  int64_t q_stride;
-  const uint16_t* k;
-  const uint16_t* v;
-  const int32_t* table;
-  int64_t table_stride;
-  const int32_t* kv_lens;
-  const int32_t* cu_rows;
-  uint16_t* o;                 // [rows][Hq][D]
-  float* lse;                  // [rows][Hq] or null
-  int rows, batch, Hq, Hkv, n_pages, page_shift, width, causal;
-  float scale_log2;            // log2(e) * scale
-};
-
-// one warp per (row, query head), keys one after another
-template <int D>
-__global__ void __launch_bounds__(128) paged_attn_simple_kernel(const __grid_constant__ PagedAttnParams p) {
-  const int lane = threadIdx.x & 31;
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (unit >= static_cast<int64_t>(p.rows) * p.Hq) return;
-  const int row = static_cast<int>(unit / p.Hq), h = static_cast<int>(unit % p.Hq);
-  int lo = 0, hi = p.batch;  // last b with cu_rows[b] <= row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (p.cu_rows[mid] <= row) lo = mid; else hi = mid;
-  }
-  const int b = lo, t0 = p.cu_rows[b], t1 = p.cu_rows[b + 1];
-  if (row < t0 || row >= t1) return;
-  const int cap = p.width << p.page_shift;
-  const int kv = min(max(p.kv_lens[b], 0), cap);
-  const int lim = p.causal ? min(kv, kv - (t1 - t0) + (row - t0) + 1) : kv;
-  constexpr int N = (D + 31) / 32;
-  float q[N], o[N];
-  const uint16_t* qs = p.q + row * p.q_stride + h * D;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    q[i] = i * 32 + lane < D ? bf16_to_f32(qs[i * 32 + lane]) : 0.f;
-    o[i] = 0.f;
-  }
-  const int g = h / (p.Hq / p.Hkv), mask = (1 << p.page_shift) - 1;
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < lim; ++j) {
-    const int page = p.table[b * p.table_stride + (j >> p.page_shift)];
-    if (page < 0 || page >= p.n_pages) continue;
-    const int64_t at = (((static_cast<int64_t>(page) * p.Hkv + g) << p.page_shift) + (j & mask)) * D;
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i * 32 + lane < D) s += q[i] * bf16_to_f32(p.k[at + i * 32 + lane]);
-    for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-    s *= p.scale_log2;
-    const float mn = fmaxf(m, s), f = m == mn ? 1.f : ex2_approx(m - mn), e = ex2_approx(s - mn);
-    l = l * f + e;
-    m = mn;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (i * 32 + lane < D) o[i] = o[i] * f + e * bf16_to_f32(p.v[at + i * 32 + lane]);
-  }
-  const float w = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-  for (int i = 0; i < N; ++i)
-    if (i * 32 + lane < D) p.o[unit * D + i * 32 + lane] = f32_to_bf16(o[i] * w);
-  if (p.lse && lane == 0) p.lse[unit] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
-}
-
 }  // namespace dg

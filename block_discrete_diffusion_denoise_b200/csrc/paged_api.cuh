@@ -3,7 +3,10 @@
 // by engine.cu, whose tensor-map helpers it uses.
 #pragma once
 
+#include <atomic>
+
 #include "paged.cuh"
+#include "paged_attention.cuh"
 
 namespace {
 
@@ -28,13 +31,90 @@ dg_status check_heads(int Hq, int Hkv, int D) {
 // a launch's own status; an error that the caller left pending is neither
 // reported nor cleared
 template <typename P>
-dg_status paged_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
+dg_status paged_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p,
+                       bool overlap = false) {
   cudaLaunchConfig_t lc{};
   lc.gridDim = grid;
   lc.blockDim = dim3(threads);
   lc.dynamicSmemBytes = smem;
   lc.stream = static_cast<cudaStream_t>(stream);
+  // start while the kernel before it still runs (the kernel waits for its end itself)
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  lc.attrs = &attr;
+  lc.numAttrs = overlap ? 1 : 0;
   return cudaLaunchKernelEx(&lc, kernel, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+// What the attention calls need of a device: its SM count, and the kernels'
+// shared-memory limits raised once (under a lock; the first call on a device
+// may come from any thread, and may be captured: neither is a stream
+// operation).
+struct PagedSetup {
+  std::atomic<int> sms{0};
+};
+PagedSetup g_paged_setup[kMaxDevices];
+std::mutex g_paged_setup_mutex;
+
+static_assert(TokCfg<64>::SMEM <= kMaxSmemPerCta && TokCfg<128>::SMEM <= kMaxSmemPerCta &&
+                  TokCfg<176>::SMEM <= kMaxSmemPerCta,
+              "token attention shared memory");
+
+template <typename K>
+bool raise_smem(K* kernel, int bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+}
+
+// SM count of the current device, 0 if it cannot be had
+int paged_device_sms() {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return 0;
+  PagedSetup& g = g_paged_setup[dev];
+  int sms = g.sms.load(std::memory_order_acquire);
+  if (sms) return sms;
+  std::lock_guard<std::mutex> lock(g_paged_setup_mutex);
+  sms = g.sms.load(std::memory_order_relaxed);
+  if (sms) return sms;
+  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+      !raise_smem(paged_token_kernel<64>, TokCfg<64>::SMEM) ||
+      !raise_smem(paged_token_kernel<128>, TokCfg<128>::SMEM) ||
+      !raise_smem(paged_token_kernel<176>, TokCfg<176>::SMEM))
+    return 0;
+  g.sms.store(sms, std::memory_order_release);
+  return sms;
+}
+
+// host checks of dg_paged_attention that need no workspace
+dg_status check_attention(const dg_paged_attention_args* a) {
+  if (!a || !a->q || !a->k_pages || !a->v_pages || !a->block_table || !a->kv_lens || !a->cu_rows || !a->out ||
+      a->n_rows < 0 || a->batch <= 0 || a->n_pages <= 0 || a->table_width <= 0 || a->table_stride < a->table_width ||
+      !(a->scale > 0.f) || !(a->scale < INFINITY) || !aligned16(a->q) || !aligned16(a->k_pages) ||
+      !aligned16(a->v_pages) || !aligned16(a->out))
+    return DG_ERR_INVALID_ARG;
+  const dg_status hs = check_heads(a->n_q_heads, a->n_kv_heads, a->head_dim);
+  if (hs != DG_OK) return hs;
+  const int shift = page_shift_of(a->page_size);
+  if (shift < 0) return DG_ERR_UNSUPPORTED;
+  if (a->q_stride < static_cast<int64_t>(a->n_q_heads) * a->head_dim || a->q_stride % 8) return DG_ERR_INVALID_ARG;
+  // TMA row coordinates and key positions are 32 bits
+  if (static_cast<int64_t>(a->n_pages) * a->n_kv_heads > (INT32_MAX >> shift) ||
+      a->table_width > (INT32_MAX >> shift))
+    return DG_ERR_CAPACITY;
+  return DG_OK;
+}
+
+constexpr int64_t paged_slot_bytes(int rows, int head_dim) { return static_cast<int64_t>(rows) * (head_dim * 4 + 8); }
+
+int64_t paged_workspace(const dg_paged_attention_args* a, int sms) {
+  return 2 * static_cast<int64_t>(sms) * paged_slot_bytes(TOK_ROWS, a->head_dim);
+}
+
+template <int D>
+dg_status launch_token(const PagedAttnParams& p, int sms, void* stream) {
+  const dg_status st = paged_launch(paged_token_kernel<D>, dim3(sms), TOK_THREADS, TokCfg<D>::SMEM, stream, p);
+  if (st != DG_OK) return st;
+  return paged_launch(paged_merge_kernel<TOK_ROWS, D>, dim3(sms), PG_MERGE_THREADS, 0, stream, p, true);
 }
 
 }  // namespace
@@ -118,30 +198,40 @@ dg_status dg_paged_append(const void* qkv, int64_t qkv_stride, int32_t n_rows, i
   return paged_launch(kern, dim3(static_cast<unsigned>(grid)), APPEND_THREADS, 0, cuda_stream, p);
 }
 
+dg_status dg_paged_attention_workspace(const dg_paged_attention_args* a, int64_t* bytes) {
+  const dg_status st = check_attention(a);
+  if (st != DG_OK || !bytes) return bytes ? st : DG_ERR_INVALID_ARG;
+  const int sms = paged_device_sms();
+  if (!sms) return DG_ERR_CUDA;
+  *bytes = paged_workspace(a, sms);
+  return DG_OK;
+}
+
 dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream) {
-  if (!a || !a->q || !a->k_pages || !a->v_pages || !a->block_table || !a->kv_lens || !a->cu_rows || !a->out ||
-      a->n_rows < 0 || a->batch <= 0 || a->n_pages <= 0 || a->table_width <= 0 || a->table_stride < a->table_width ||
-      !(a->scale > 0.f) || !(a->scale < INFINITY) || !aligned16(a->q) || !aligned16(a->k_pages) ||
-      !aligned16(a->v_pages) || !aligned16(a->out))
-    return DG_ERR_INVALID_ARG;
-  const dg_status hs = check_heads(a->n_q_heads, a->n_kv_heads, a->head_dim);
-  if (hs != DG_OK) return hs;
-  const int shift = page_shift_of(a->page_size);
-  if (shift < 0) return DG_ERR_UNSUPPORTED;
-  if (a->q_stride < static_cast<int64_t>(a->n_q_heads) * a->head_dim || a->q_stride % 8) return DG_ERR_INVALID_ARG;
-  if (a->n_pages > (INT32_MAX >> shift) || a->table_width > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;
+  const dg_status cs = check_attention(a);
+  if (cs != DG_OK) return cs;
   if (a->n_rows == 0) return DG_OK;
+  if (!a->workspace || !aligned16(a->workspace)) return DG_ERR_INVALID_ARG;
+  const int sms = paged_device_sms();
+  if (!sms) return DG_ERR_CUDA;
+  if (a->workspace_bytes < paged_workspace(a, sms)) return DG_ERR_CAPACITY;
+  const int shift = page_shift_of(a->page_size);
   PagedAttnParams p;
+  const uint64_t pool_rows = (static_cast<uint64_t>(a->n_pages) * a->n_kv_heads) << shift;
+  const uint32_t box = std::min(a->page_size, PG_BK);
+  if (!make_map(&p.k_map, a->k_pages, pool_rows, a->head_dim, box) ||
+      !make_map(&p.v_map, a->v_pages, pool_rows, a->head_dim, box))
+    return DG_ERR_CUDA;
   p.q = static_cast<const uint16_t*>(a->q);
   p.q_stride = a->q_stride;
-  p.k = static_cast<const uint16_t*>(a->k_pages);
-  p.v = static_cast<const uint16_t*>(a->v_pages);
   p.table = a->block_table;
   p.table_stride = a->table_stride;
   p.kv_lens = a->kv_lens;
   p.cu_rows = a->cu_rows;
   p.o = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
+  p.part = static_cast<float*>(a->workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part + 2 * static_cast<int64_t>(sms) * TOK_ROWS * a->head_dim);
   p.rows = a->n_rows;
   p.batch = a->batch;
   p.Hq = a->n_q_heads;
@@ -151,10 +241,12 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   p.width = a->table_width;
   p.causal = a->causal != 0;
   p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
-  const int64_t units = static_cast<int64_t>(a->n_rows) * a->n_q_heads;
-  auto* kern = a->head_dim == 64 ? paged_attn_simple_kernel<64>
-               : a->head_dim == 128 ? paged_attn_simple_kernel<128> : paged_attn_simple_kernel<176>;
-  return paged_launch(kern, dim3(static_cast<unsigned>((units + 3) / 4)), 128, 0, cuda_stream, p);
+  p.err = DevErr{nullptr, 1000000000ull};
+  switch (a->head_dim) {
+    case 64: return launch_token<64>(p, sms, cuda_stream);
+    case 128: return launch_token<128>(p, sms, cuda_stream);
+    default: return launch_token<176>(p, sms, cuda_stream);
+  }
 }
 
 }  // extern "C"

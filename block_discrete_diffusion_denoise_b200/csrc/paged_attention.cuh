@@ -1,0 +1,593 @@
+// Attention of packed rows over paged keys and values.  Row i of request b (n
+// rows, kv keys) sees keys [0, kv), or with `causal` [0, kv - n + i + 1):
+//   o = softmax(scale q K^T) V over them, lse = log sum exp of its scores.
+// Keys of a page id outside the pool count as masked; a row that sees nothing
+// gives zeros and lse = -inf.
+//
+// Work is counted in units: one 64-key block of one tile (packed rows of one
+// request and kv head).  The units of a call form one line, in the order
+// (request, row tile, kv head, key block), and CTA c of N takes the stretch
+// [W c / N, W (c + 1) / N): every CTA has the same work whatever the lengths,
+// and the lengths are read on the device, so a captured launch serves any.  A
+// tile that a stretch cuts leaves its raw rows and row statistics in a
+// partial slot (two per CTA: the stretch's first tile and its last), and
+// the merge kernel joins them in key order.
+#pragma once
+
+#include "paged.cuh"
+
+namespace dg {
+
+constexpr int PG_BK = 64;      // keys per unit
+
+struct PagedAttnParams {
+  CUtensorMap k_map;           // 2-D (D, n_pages * Hkv * page_size) over the pool; box (64, min(page_size, 64))
+  CUtensorMap v_map;
+  const uint16_t* q;           // [rows][Hq][D], row stride q_stride
+  int64_t q_stride;
+  const int32_t* table;
+  int64_t table_stride;
+  const int32_t* kv_lens;
+  const int32_t* cu_rows;
+  uint16_t* o;                 // [rows][Hq][D]
+  float* lse;                  // [rows][Hq] or null
+  float* part;                 // [CTA][2][tile rows][D] raw rows of cut tiles
+  float2* part_ml;             // [CTA][2][tile rows] their (max in log2 units, sum)
+  int rows, batch, Hq, Hkv, n_pages, page_shift, width, causal;
+  float scale_log2;            // log2(e) * scale
+  DevErr err;
+};
+
+struct PagedRequest {
+  int t0, n, kv, nb, tiles;    // first row, rows, keys, key blocks of a tile, row tiles
+};
+
+template <int ROWS>
+__device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams& p, int b) {
+  PagedRequest r;
+  r.t0 = min(max(p.cu_rows[b], 0), p.rows);
+  r.n = max(min(p.cu_rows[b + 1], p.rows) - r.t0, 0);
+  r.kv = min(max(p.kv_lens[b], 0), p.width << p.page_shift);
+  r.nb = r.kv > 0 ? (r.kv - 1) / PG_BK + 1 : 1;   // a tile without keys still writes its rows
+  r.tiles = (r.n * (p.Hq / p.Hkv) + ROWS - 1) / ROWS;
+  return r;
+}
+
+// a CTA's stretch [lo, hi) of the line's `total` units, and where it starts:
+// `rem` units into request b.  With fewer units than CTAs only the first
+// `ctas` = total have one each.
+struct PagedRange {
+  int64_t lo, hi, rem, total;
+  int b, ctas;
+};
+
+// One pass over the batch by the whole CTA: each thread sums the units of a
+// run of requests, a scan gives their places on the line.
+template <int ROWS>
+__device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int cta, int ctas) {
+  __shared__ long long warp_sum[32];
+  __shared__ long long found_rem;
+  __shared__ int found_b;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  const int per = (p.batch + blockDim.x - 1) / blockDim.x;
+  const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
+  long long sum = 0;
+  for (int b = b0; b < b1; ++b) {
+    const PagedRequest r = paged_request<ROWS>(p, b);
+    sum += static_cast<long long>(r.tiles) * p.Hkv * r.nb;
+  }
+  long long upto = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += x;
+  }
+  if (lane == 31) warp_sum[warp] = upto;
+  __syncthreads();
+  long long total = 0, before = 0;
+  for (int w = 0; w < warps; ++w) {
+    if (w < warp) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+  PagedRange g;
+  g.total = total;
+  g.ctas = static_cast<int>(min64(ctas, total));
+  g.lo = cta < g.ctas ? total * cta / g.ctas : total;
+  g.hi = cta < g.ctas ? total * (cta + 1) / g.ctas : total;
+  long long at = before + upto - sum;
+  if (g.lo < g.hi && g.lo >= at && g.lo < at + sum) {
+    for (int b = b0; b < b1; ++b) {
+      const PagedRequest r = paged_request<ROWS>(p, b);
+      const long long u = static_cast<long long>(r.tiles) * p.Hkv * r.nb;
+      if (g.lo < at + u) {
+        found_b = b;
+        found_rem = g.lo - at;
+        break;
+      }
+      at += u;
+    }
+  }
+  __syncthreads();
+  g.b = g.lo < g.hi ? found_b : p.batch;
+  g.rem = found_rem;
+  return g;
+}
+
+// Walks the tiles of a stretch: the key blocks [kb0, kb1) of row tile `tile`
+// of kv head h of request b.
+template <int ROWS>
+struct PagedWalk {
+  PagedRequest r;
+  int64_t left;
+  int b, tile, h, kb0, kb1;
+
+  __device__ __forceinline__ PagedWalk(const PagedAttnParams& p, const PagedRange& g) : left(g.hi - g.lo), b(g.b) {
+    if (left <= 0) return;
+    r = paged_request<ROWS>(p, b);
+    const int64_t t = g.rem / r.nb;
+    tile = static_cast<int>(t / p.Hkv);
+    h = static_cast<int>(t % p.Hkv);
+    kb0 = static_cast<int>(g.rem % r.nb);
+    kb1 = static_cast<int>(min64(r.nb, kb0 + left));
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool whole() const { return kb0 == 0 && kb1 == r.nb; }
+  __device__ __forceinline__ void next(const PagedAttnParams& p) {
+    left -= kb1 - kb0;
+    if (left <= 0) return;
+    kb0 = 0;
+    if (++h == p.Hkv) {
+      h = 0;
+      if (++tile == r.tiles) {
+        tile = 0;
+        do {
+          if (++b >= p.batch) {   // lengths that changed under the call
+            left = 0;
+            return;
+          }
+          r = paged_request<ROWS>(p, b);
+        } while (r.tiles == 0);
+      }
+    }
+    kb1 = static_cast<int>(min64(r.nb, left));
+  }
+};
+
+// untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
+__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(smem_dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
+// c (16 x 8, fp32) += a (16 x 16) b (16 x 8), bf16
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// ----------------------------------------------------------------------------
+// Few rows per request (single tokens): tiles of 16 packed rows (row = i * G +
+// query head of the group), so that the G heads of a group share one read of
+// their keys.
+//
+// Bound by HBM: 4 D bytes per key and kv head against 2 x 16 x 2 D operations,
+// of which a token's G rows are useful.  So the products run on mma.sync
+// (64 x 16 x 2 D x 2 per block, under a tenth of the block's time on the
+// memory), and everything else serves the stream of pages: one producer warp
+// keeps TOK_STAGES blocks of K and V in flight, each landing swizzled by TMA
+// so that ldmatrix reads it without bank conflicts; four warps take 16 of its
+// 64 keys each, with running maxima, sums and rows of their own (no barrier
+// between them inside a tile), joined through shared memory at a tile's end.
+// ----------------------------------------------------------------------------
+constexpr int TOK_ROWS = 16;
+constexpr int TOK_WARPS = 4;                       // consumer warps
+constexpr int TOK_THREADS = 32 * (1 + TOK_WARPS);
+
+template <int D>
+struct TokCfg {
+  static constexpr int DK = (D + 63) / 64;
+  static constexpr int KV_BYTES = DK * PG_BK * 128;             // K or V of a block
+  static constexpr int STAGES = D == 64 ? 6 : D == 128 ? 4 : 3;
+  static constexpr int Q_BYTES = TOK_ROWS * D * 2;
+  static constexpr int Q_BUFS = STAGES + 1;                     // a tile's rows arrive with its first block
+  static constexpr int O_LD = D + 4;
+  static constexpr int O_BYTES = TOK_WARPS * TOK_ROWS * O_LD * 4;
+  static constexpr int O_OFF = STAGES * 2 * KV_BYTES;
+  static constexpr int Q_OFF = O_OFF + O_BYTES;
+  static constexpr int TAIL_OFF = (Q_OFF + Q_BUFS * Q_BYTES + 127) / 128 * 128;
+  static constexpr int SMEM = 1024 + TAIL_OFF + 1536;
+};
+
+enum TokFlags : int { TOK_FIRST = 1, TOK_LAST = 2, TOK_EXIT = 4, TOK_WHOLE = 8, TOK_SLOT1 = 16 };
+
+// what the consumers need to know of a stage
+struct TokDesc {
+  uint64_t valid;              // keys of the block in pages of the pool, below kv
+  int flags, qbuf;
+  int t0, n, kv, h;
+  int row0;                    // first packed row of the tile
+  int key0;                    // first key of the block
+};
+
+// (row, column) of a tile's live rows -> the output row
+__device__ __forceinline__ int64_t paged_out_row(const PagedAttnParams& p, int t0, int packed, int h) {
+  const int G = p.Hq / p.Hkv;
+  return static_cast<int64_t>(t0 + packed / G) * p.Hq + h * G + packed % G;
+}
+
+// NaN in every row a stretch should have written (a wait ran out)
+template <int ROWS, int D>
+__device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
+  int seg = 0;
+  for (PagedWalk<ROWS> w(p, g); w.more(); w.next(p), ++seg) {
+    const int live = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
+    for (int i = threadIdx.x; i < live * D; i += blockDim.x) {
+      const int64_t out = paged_out_row(p, w.r.t0, w.tile * ROWS + i / D, w.h);
+      if (w.whole()) {
+        p.o[out * D + i % D] = 0x7fc0;
+        if (p.lse) p.lse[out] = NAN;
+      } else {
+        const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0)) * ROWS + i / D;
+        p.part[slot * D + i % D] = NAN;
+        p.part_ml[slot] = make_float2(0.f, NAN);
+      }
+    }
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __grid_constant__ PagedAttnParams p) {
+  DG_TIMELINE_SCOPE(TLK_ATTENTION);
+  using C = TokCfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* s_o = reinterpret_cast<float*>(smem + C::O_OFF);       // [warp][16][O_LD]
+  uint8_t* s_q = smem + C::Q_OFF;
+  uint8_t* tail = smem + C::TAIL_OFF;
+  uint64_t* full = reinterpret_cast<uint64_t*>(tail);
+  uint64_t* empty = full + C::STAGES;
+  uint64_t* o_full = empty + C::STAGES;                         // all four warps' rows of a tile written
+  uint64_t* o_free = o_full + 1;                                // ... and read again
+  TokDesc* desc = reinterpret_cast<TokDesc*>(tail + 256);       // [STAGES]
+  float2* s_ml = reinterpret_cast<float2*>(tail + 768);         // [warp][16]
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 1280);
+  static_assert(C::STAGES * sizeof(TokDesc) <= 512 && (2 * C::STAGES + 2) * 8 <= 256, "tail layout");
+  static_assert(TOK_WARPS * TOK_ROWS * sizeof(float2) == 512, "tail layout");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tma_prefetch_desc(&p.k_map);
+    tma_prefetch_desc(&p.v_map);
+    for (int s = 0; s < C::STAGES; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], TOK_WARPS);
+    }
+    mbar_init(o_full, TOK_WARPS);
+    mbar_init(o_free, TOK_WARPS);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  pdl_launch_dependents();
+  const PagedRange g = paged_range<TOK_ROWS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
+  const int G = p.Hq / p.Hkv;
+  bool ok = true;
+
+  if (warp == 0) {
+    // ------------------------------- producer -------------------------------
+    const int box = min(1 << p.page_shift, PG_BK);              // keys per TMA box
+    const int pieces = PG_BK / box;                             // pages (or part of one) per block
+    const int rows_per_page = p.Hkv << p.page_shift;
+    const int my_piece = lane % pieces, my_col = lane / pieces; // box of this lane: K columns, then V columns
+    const bool mine = my_col < 2 * C::DK;
+    const bool is_v = my_col >= C::DK;
+    const int db = is_v ? my_col - C::DK : my_col;
+    const uint64_t pol = policy_evict_first();
+    int it = 0, seg = 0;
+    uint32_t issued = 0, par = 0;
+    for (PagedWalk<TOK_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+      const int32_t* tab = p.table + w.b * p.table_stride;
+      const int live = min(w.r.n * G - w.tile * TOK_ROWS, TOK_ROWS);
+      int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
+      for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
+        const int s = it % C::STAGES;
+        const int first_page = (kb * PG_BK) >> p.page_shift;
+        if (ids0 < 0 || first_page + pieces > ids0 + 32) {
+          ids0 = first_page;
+          ids = ids0 + lane < p.width ? tab[ids0 + lane] : -1;
+        }
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err) && !*abort_flag);
+        if (!ok) break;
+        const int page = __shfl_sync(0xffffffffu, ids, first_page + my_piece - ids0);
+        const int key = kb * PG_BK + my_piece * box;
+        const bool good = page >= 0 && page < p.n_pages && key < w.r.kv;
+        // lanes 0 .. pieces-1 hold one piece each
+        const uint32_t pmask = __ballot_sync(0xffffffffu, good && lane < pieces);
+        uint8_t* stage = smem + s * 2 * C::KV_BYTES;
+        if (lane == 0) {
+          uint64_t valid = 0;
+          for (int i = 0; i < pieces; ++i)
+            if (pmask >> i & 1) valid |= (box == 64 ? ~uint64_t(0) : ((uint64_t(1) << box) - 1)) << (i * box);
+          const int keys = w.r.kv - kb * PG_BK;
+          if (keys < PG_BK) valid &= keys > 0 ? (uint64_t(1) << keys) - 1 : 0;
+          const bool first = kb == w.kb0;
+          TokDesc d;
+          d.valid = valid;
+          d.flags = (first ? TOK_FIRST : 0) | (kb + 1 == w.kb1 ? TOK_LAST : 0) | (w.whole() ? TOK_WHOLE : 0) |
+                    (seg > 0 ? TOK_SLOT1 : 0);
+          d.qbuf = seg % C::Q_BUFS;
+          d.t0 = w.r.t0;
+          d.n = w.r.n;
+          d.kv = w.r.kv;
+          d.h = w.h;
+          d.row0 = w.tile * TOK_ROWS;
+          d.key0 = kb * PG_BK;
+          desc[s] = d;
+          mbar_arrive_expect_tx(&full[s], __popc(pmask) * box * 128 * 2 * C::DK + (first ? live * D * 2 : 0));
+        }
+        __syncwarp();
+        if (mine && good) {
+          const int off = key & ((1 << p.page_shift) - 1);
+          tma_load_2d(stage + (is_v ? C::KV_BYTES : 0) + db * PG_BK * 128 + my_piece * box * 128,
+                      is_v ? &p.v_map : &p.k_map, &full[s], db * 64,
+                      page * rows_per_page + (w.h << p.page_shift) + off, pol);
+        }
+        if (kb == w.kb0 && lane < live) {
+          const int r = w.tile * TOK_ROWS + lane;
+          bulk_load(s_q + (seg % C::Q_BUFS) * C::Q_BYTES + lane * D * 2,
+                    p.q + (w.r.t0 + r / G) * p.q_stride + (w.h * G + r % G) * D, D * 2, &full[s]);
+        }
+        issued |= 1u << s;
+        par = (par & ~(1u << s)) | (((it / C::STAGES) & 1) << s);
+      }
+    }
+    if (lane == 0) {
+      const int s = it % C::STAGES;
+      if (ok && mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err)) {
+        desc[s].flags = TOK_EXIT;
+        mbar_arrive(&full[s]);
+      } else {
+        *abort_flag = 1;
+        // every copy issued here lands before the CTA exits
+        for (int x = 0; x < C::STAGES; ++x)
+          if (issued >> x & 1) mbar_wait(&full[x], par >> x & 1, p.err);
+      }
+    }
+  } else {
+    // ------------------------------- consumers ------------------------------
+    const int w = warp - 1, gr = lane >> 2, c = lane & 3, mi = lane >> 3, mr = lane & 7;
+    uint32_t qf[D / 16][4];
+    float o[D / 8][4];
+    float m[2], l[2];
+    int lim[2] = {0, 0};
+    int seg = 0;
+    for (int it = 0;; ++it) {
+      const int s = it % C::STAGES;
+      ok = __all_sync(0xffffffffu, mbar_wait(&full[s], (it / C::STAGES) & 1, p.err) && !*abort_flag);
+      if (!ok) break;
+      const TokDesc d = desc[s];
+      if (d.flags & TOK_EXIT) break;
+      const uint32_t k_at = smem_u32(smem + s * 2 * C::KV_BYTES), v_at = k_at + C::KV_BYTES;
+      if (d.flags & TOK_FIRST) {
+        const uint32_t q_at = smem_u32(s_q + d.qbuf * C::Q_BYTES);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk)
+          ldmatrix_x4(qf[kk], q_at + ((mi & 1) * 8 + mr) * (D * 2) + kk * 32 + (mi >> 1) * 16);
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          m[x] = -INFINITY;
+          l[x] = 0.f;
+          lim[x] = p.causal ? min(d.kv, d.kv - d.n + (d.row0 + gr + 8 * x) / G + 1) : d.kv;
+        }
+      }
+      // S = Q K^T for this warp's 16 keys: two 16 x 8 tiles
+      float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        uint32_t kf[4];
+        ldmatrix_x4(kf, k_at + (kk >> 2) * (PG_BK * 128) + (w * 16 + (mi >> 1) * 8 + mr) * 128 +
+                            ((((kk & 3) * 2 + (mi & 1)) ^ mr) << 4));
+        mma_16816(sc[0], qf[kk], kf[0], kf[1]);
+        mma_16816(sc[1], qf[kk], kf[2], kf[3]);
+      }
+      const uint32_t valid = static_cast<uint32_t>(d.valid >> (w * 16)) & 0xffffu;
+      const int rel = d.key0 + w * 16;
+      uint32_t pf[4];
+      float f[2];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        float mx = -INFINITY;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = t * 8 + 2 * c + e;
+            float& v = sc[t][2 * x + e];
+            v = (valid >> key & 1) && rel + key < lim[x] ? v * p.scale_log2 : -INFINITY;
+            mx = fmaxf(mx, v);
+          }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const float mn = fmaxf(m[x], mx), base = mn == -INFINITY ? 0.f : mn;
+        f[x] = ex2_approx(m[x] - base);
+        m[x] = mn;
+        float sum = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          // p enters the second product in bf16 (2^-9 of each, averaging out over keys); its sum stays fp32
+          const float p0 = ex2_approx(sc[t][2 * x] - base), p1 = ex2_approx(sc[t][2 * x + 1] - base);
+          sum += p0 + p1;
+          pf[2 * t + x] = pack_bf16x2(p0, p1);
+        }
+        l[x] = l[x] * f[x] + sum;
+      }
+      if (__any_sync(0xffffffffu, f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+          o[t][0] *= f[0];
+          o[t][1] *= f[0];
+          o[t][2] *= f[1];
+          o[t][3] *= f[1];
+        }
+      }
+      // O += P V; values of masked keys may be anything, so they are cleared
+      const bool clear = valid != 0xffffu;
+      const uint32_t keep0 = (valid >> (2 * c) & 1 ? 0xffffu : 0u) | (valid >> (2 * c + 1) & 1 ? 0xffff0000u : 0u);
+      const uint32_t keep1 = (valid >> (2 * c + 8) & 1 ? 0xffffu : 0u) | (valid >> (2 * c + 9) & 1 ? 0xffff0000u : 0u);
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t) {
+        uint32_t vf[4];
+        ldmatrix_x4_trans(vf, v_at + (t >> 2) * (PG_BK * 128) + (w * 16 + (mi & 1) * 8 + mr) * 128 +
+                                  ((((t & 3) * 2 + (mi >> 1)) ^ mr) << 4));
+        if (clear) {
+          vf[0] &= keep0;
+          vf[1] &= keep1;
+          vf[2] &= keep0;
+          vf[3] &= keep1;
+        }
+        mma_16816(o[2 * t], pf, vf[0], vf[1]);
+        mma_16816(o[2 * t + 1], pf, vf[2], vf[3]);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty[s]);
+      if (!(d.flags & TOK_LAST)) continue;
+
+      // -------- the tile's end: the four warps' rows joined in order --------
+      const int live = min(d.n * G - d.row0, TOK_ROWS);
+      if (seg > 0) {
+        ok = __all_sync(0xffffffffu, mbar_wait(o_free, (seg - 1) & 1, p.err) && !*abort_flag);
+        if (!ok) break;
+      }
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
+        l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
+        const int r = gr + 8 * x;
+        if (r < live) {
+          if (c == 0) s_ml[w * TOK_ROWS + r] = make_float2(m[x], l[x]);
+          float* dst = s_o + (w * TOK_ROWS + r) * C::O_LD + 2 * c;
+#pragma unroll
+          for (int t = 0; t < D / 8; ++t) *reinterpret_cast<float2*>(dst + t * 8) = make_float2(o[t][2 * x], o[t][2 * x + 1]);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_full);
+      ok = __all_sync(0xffffffffu, mbar_wait(o_full, seg & 1, p.err) && !*abort_flag);
+      if (!ok) break;
+      const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (d.flags & TOK_SLOT1 ? 1 : 0)) * TOK_ROWS;
+      for (int i = threadIdx.x - 32; i < live * (D / 4); i += 32 * TOK_WARPS) {
+        const int r = i / (D / 4), c4 = i % (D / 4) * 4;
+        float M = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < TOK_WARPS; ++x) M = fmaxf(M, s_ml[x * TOK_ROWS + r].x);
+        const float base = M == -INFINITY ? 0.f : M;
+        float L = 0.f;
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int x = 0; x < TOK_WARPS; ++x) {
+          const float2 ml = s_ml[x * TOK_ROWS + r];
+          const float e = ex2_approx(ml.x - base);
+          const float4 v = *reinterpret_cast<const float4*>(s_o + (x * TOK_ROWS + r) * C::O_LD + c4);
+          L += e * ml.y;
+          a.x += e * v.x;
+          a.y += e * v.y;
+          a.z += e * v.z;
+          a.w += e * v.w;
+        }
+        if (d.flags & TOK_WHOLE) {
+          const float inv = L == 0.f ? 0.f : 1.f / L;
+          const int64_t row = paged_out_row(p, d.t0, d.row0 + r, d.h);
+          *reinterpret_cast<uint2*>(p.o + row * D + c4) =
+              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+          if (p.lse && c4 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+        } else {
+          *reinterpret_cast<float4*>(p.part + (slot + r) * D + c4) = a;
+          if (c4 == 0) p.part_ml[slot + r] = make_float2(M, L);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+      ++seg;
+    }
+    if (!ok) *abort_flag = 1;
+  }
+  __syncthreads();
+  if (*abort_flag) paged_poison<TOK_ROWS, D>(p, g);
+}
+
+// ----------------------------------------------------------------------------
+// Joins the tiles that the stretches cut.  CTA c takes the tile that starts
+// in stretch c and ends behind it, if there is one:
+//   o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i
+// over its pieces in key order.  Launched with the attention kernel still
+// running, so its own start and scan of the batch cost nothing.
+// ----------------------------------------------------------------------------
+constexpr int PG_MERGE_THREADS = 256;
+
+template <int ROWS, int D>
+__global__ void __launch_bounds__(PG_MERGE_THREADS) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
+  DG_TIMELINE_SCOPE(TLK_ATTN_MERGE);
+  const PagedRange g = paged_range<ROWS>(p, blockIdx.x, gridDim.x);
+  PagedWalk<ROWS> w(p, g);
+  int seg = 0;
+  while (w.more() && w.left > w.kb1 - w.kb0) {
+    w.next(p);
+    ++seg;
+  }
+  const bool cut = w.more() && w.kb0 == 0 && w.kb1 < w.r.nb;   // the stretch's last tile goes on behind it
+  pdl_wait();
+  if (!cut) return;
+  const int live = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
+  const int64_t end = g.hi - w.kb1 + w.r.nb;                    // the tile's end on the line
+  // the pieces behind this CTA's are the first of each stretch up to the one that holds unit end - 1
+  // (floor(W c / N) <= u is c <= ((u + 1) N - 1) / W)
+  const int last = static_cast<int>((end * g.ctas - 1) / g.total);
+  for (int i = threadIdx.x; i < live * (D / 4); i += PG_MERGE_THREADS) {
+    const int r = i / (D / 4), c4 = i % (D / 4) * 4;
+    int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0)) * ROWS + r;
+    float2 ml = p.part_ml[slot];
+    float4 a = *reinterpret_cast<const float4*>(p.part + slot * D + c4);
+    float M = ml.x, L = ml.y;
+    for (int x = blockIdx.x + 1; x <= last; ++x) {
+      slot = static_cast<int64_t>(x) * 2 * ROWS + r;
+      ml = p.part_ml[slot];
+      const float4 v = *reinterpret_cast<const float4*>(p.part + slot * D + c4);
+      const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
+      const float e0 = ex2_approx(M - base), e1 = ex2_approx(ml.x - base);
+      L = L * e0 + ml.y * e1;
+      a.x = a.x * e0 + v.x * e1;
+      a.y = a.y * e0 + v.y * e1;
+      a.z = a.z * e0 + v.z * e1;
+      a.w = a.w * e0 + v.w * e1;
+      M = mn;
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t row = paged_out_row(p, w.r.t0, w.tile * ROWS + r, w.h);
+    *reinterpret_cast<uint2*>(p.o + row * D + c4) =
+        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+    if (p.lse && c4 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+  }
+}
+
+}  // namespace dg

@@ -482,7 +482,11 @@ dg_status dg_paged_append(const void* qkv_dev, int64_t qkv_stride, int32_t n_row
  *   causal      0: every row sees all keys of its request; 1: row i of n sees
  *               keys [0, kv_lens - n + i]
  *   max_rows    an upper bound of the rows of one request, or 0 (n_rows): it
- *               picks the kernel, the result does not depend on it */
+ *               picks the kernel (a wrong one costs time, not the result)
+ *   workspace   device memory, 16-byte aligned, of at least
+ *               dg_paged_attention_workspace bytes; its contents do not matter
+ *               before the call and mean nothing after it.  Calls that may
+ *               overlap on the GPU need one each */
 typedef struct dg_paged_attention_args {
   const void* q;
   const void* k_pages;
@@ -492,6 +496,8 @@ typedef struct dg_paged_attention_args {
   const int32_t* cu_rows;
   void* out;
   float* lse;
+  void* workspace;
+  int64_t workspace_bytes;
   int64_t q_stride;
   int64_t table_stride;
   int32_t n_rows;
@@ -507,14 +513,20 @@ typedef struct dg_paged_attention_args {
   float scale;
 } dg_paged_attention_args;
 
+/* Workspace bytes of a call with these arguments (workspace and
+ * workspace_bytes are not looked at); they depend on the device, the head
+ * dimension, the group size and max_rows (n_rows) alone, not on any length. */
+dg_status dg_paged_attention_workspace(const dg_paged_attention_args* args, int64_t* bytes);
+
 /* Attention of packed rows over their requests' pages (codemajin.net
  * "DiffusionGemma architecture", section 3.2: a canvas over the cache and
  * itself, or the causal encoder), for anything from one row per request to
  * whole prompts.  Rows outside [cu_rows[0], cu_rows[batch]) are left as they
  * were; cu_rows must not decrease.  Keys beyond table_width pages, and keys of
  * a page id outside the pool, are masked; a row that sees no key gets zeros
- * and lse = -inf.  What lies in the pages at masked positions (NaN included)
- * has no effect. */
+ * and lse = -inf.  What lies in the pages behind a request's keys (NaN
+ * included) has no effect.  If a bounded wait inside the kernel ran out, the
+ * rows it should have computed come back NaN. */
 dg_status dg_paged_attention(const dg_paged_attention_args* args, void* cuda_stream);
 
 #ifdef __cplusplus

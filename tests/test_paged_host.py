@@ -64,7 +64,8 @@ def test_append_refuses(kw, status):
 
 
 def attention(**kw):
-    a = dict(q=A, k_pages=A, v_pages=A, block_table=A, kv_lens=A, cu_rows=A, out=A, lse=None, q_stride=2816,
+    a = dict(q=A, k_pages=A, v_pages=A, block_table=A, kv_lens=A, cu_rows=A, out=A, lse=None, workspace=None,
+             workspace_bytes=0, q_stride=2816,
              table_stride=8, n_rows=4, batch=2, n_q_heads=16, n_kv_heads=8, head_dim=176, n_pages=10, page_size=64,
              table_width=8, causal=0, max_rows=0, scale=0.1)
     a.update(kw)
@@ -79,7 +80,8 @@ def attention(**kw):
     (dict(k_pages=A + 8), 1), (dict(v_pages=A + 8), 1), (dict(out=A + 8), 1), (dict(q_stride=2815), 1),
     (dict(q_stride=2820), 1), (dict(n_q_heads=0), 1), (dict(head_dim=80), 7), (dict(n_q_heads=17), 7),
     (dict(n_q_heads=24, q_stride=8000), 7), (dict(page_size=8), 7), (dict(n_pages=2 ** 25), 3),
-    (dict(table_width=2 ** 25, table_stride=2 ** 25), 3), (dict(n_rows=0), 0),
+    (dict(n_pages=2 ** 23), 3), (dict(table_width=2 ** 25, table_stride=2 ** 25), 3), (dict(n_rows=0), 0),
+    (dict(), 1), (dict(workspace=A + 8, workspace_bytes=2 ** 40), 1),
 ])
 def test_attention_refuses(kw, status):
     assert attention(**kw) == status
