@@ -7,6 +7,7 @@
 
 #include "paged.cuh"
 #include "paged_attention.cuh"
+#include "paged_canvas.cuh"
 
 namespace {
 
@@ -60,6 +61,9 @@ std::mutex g_paged_setup_mutex;
 static_assert(TokCfg<64>::SMEM <= kMaxSmemPerCta && TokCfg<128>::SMEM <= kMaxSmemPerCta &&
                   TokCfg<176>::SMEM <= kMaxSmemPerCta,
               "token attention shared memory");
+static_assert(CvCfg<64>::SMEM <= kMaxSmemPerCta && CvCfg<128>::SMEM <= kMaxSmemPerCta &&
+                  CvCfg<176>::SMEM <= kMaxSmemPerCta,
+              "canvas attention shared memory");
 
 template <typename K>
 bool raise_smem(K* kernel, int bytes) {
@@ -79,7 +83,10 @@ int paged_device_sms() {
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
       !raise_smem(paged_token_kernel<64>, TokCfg<64>::SMEM) ||
       !raise_smem(paged_token_kernel<128>, TokCfg<128>::SMEM) ||
-      !raise_smem(paged_token_kernel<176>, TokCfg<176>::SMEM))
+      !raise_smem(paged_token_kernel<176>, TokCfg<176>::SMEM) ||
+      !raise_smem(paged_canvas_kernel<64>, CvCfg<64>::SMEM) ||
+      !raise_smem(paged_canvas_kernel<128>, CvCfg<128>::SMEM) ||
+      !raise_smem(paged_canvas_kernel<176>, CvCfg<176>::SMEM))
     return 0;
   g.sms.store(sms, std::memory_order_release);
   return sms;
@@ -104,10 +111,31 @@ dg_status check_attention(const dg_paged_attention_args* a) {
   return DG_OK;
 }
 
-constexpr int64_t paged_slot_bytes(int rows, int head_dim) { return static_cast<int64_t>(rows) * (head_dim * 4 + 8); }
+// Tiles of 16 packed rows for requests whose rows fit one (they are bound by
+// the stream of pages), of 256 on the tensor cores' accumulators above it.
+bool few_rows(const dg_paged_attention_args* a) {
+  const int rows = a->max_rows > 0 && a->max_rows < a->n_rows ? a->max_rows : a->n_rows;
+  return static_cast<int64_t>(rows) * (a->n_q_heads / a->n_kv_heads) <= TOK_ROWS;
+}
 
 int64_t paged_workspace(const dg_paged_attention_args* a, int sms) {
-  return 2 * static_cast<int64_t>(sms) * paged_slot_bytes(TOK_ROWS, a->head_dim);
+  const int64_t rows = few_rows(a) ? TOK_ROWS : CV_ROWS;
+  return 2 * sms * rows * (a->head_dim * 4 + 8);
+}
+
+// Queries [row][Hq][D] seen as (D, G, Hkv, row): a box of 64 columns x G heads
+// x 1 kv head x 128 / G rows is the 128 packed rows of one GQA group.
+bool make_map_rows(CUtensorMap* m, const dg_paged_attention_args* a) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return false;
+  const cuuint64_t D = a->head_dim, G = a->n_q_heads / a->n_kv_heads;
+  cuuint64_t dims[4] = {D, G, static_cast<cuuint64_t>(a->n_kv_heads), static_cast<cuuint64_t>(a->n_rows)};
+  cuuint64_t strides[3] = {D * 2, G * D * 2, static_cast<cuuint64_t>(a->q_stride) * 2};
+  cuuint32_t box[4] = {64, static_cast<cuuint32_t>(G), 1, static_cast<cuuint32_t>(CV_TILE / G)};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(a->q), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int D>
@@ -115,6 +143,13 @@ dg_status launch_token(const PagedAttnParams& p, int sms, void* stream) {
   const dg_status st = paged_launch(paged_token_kernel<D>, dim3(sms), TOK_THREADS, TokCfg<D>::SMEM, stream, p);
   if (st != DG_OK) return st;
   return paged_launch(paged_merge_kernel<TOK_ROWS, D>, dim3(sms), PG_MERGE_THREADS, 0, stream, p, true);
+}
+
+template <int D>
+dg_status launch_canvas(const CanvasParams& p, int sms, void* stream) {
+  const dg_status st = paged_launch(paged_canvas_kernel<D>, dim3(sms), CV_THREADS, CvCfg<D>::SMEM, stream, p);
+  if (st != DG_OK) return st;
+  return paged_launch(paged_merge_kernel<CV_ROWS, D>, dim3(sms, 8), PG_MERGE_THREADS, 0, stream, p.a, true);
 }
 
 }  // namespace
@@ -216,11 +251,13 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   if (!sms) return DG_ERR_CUDA;
   if (a->workspace_bytes < paged_workspace(a, sms)) return DG_ERR_CAPACITY;
   const int shift = page_shift_of(a->page_size);
-  PagedAttnParams p;
+  CanvasParams cp;
+  PagedAttnParams& p = cp.a;
+  const bool few = few_rows(a);
   const uint64_t pool_rows = (static_cast<uint64_t>(a->n_pages) * a->n_kv_heads) << shift;
   const uint32_t box = std::min(a->page_size, PG_BK);
   if (!make_map(&p.k_map, a->k_pages, pool_rows, a->head_dim, box) ||
-      !make_map(&p.v_map, a->v_pages, pool_rows, a->head_dim, box))
+      !make_map(&p.v_map, a->v_pages, pool_rows, a->head_dim, box) || (!few && !make_map_rows(&cp.q_map, a)))
     return DG_ERR_CUDA;
   p.q = static_cast<const uint16_t*>(a->q);
   p.q_stride = a->q_stride;
@@ -231,7 +268,7 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   p.o = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
   p.part = static_cast<float*>(a->workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part + 2 * static_cast<int64_t>(sms) * TOK_ROWS * a->head_dim);
+  p.part_ml = reinterpret_cast<float2*>(p.part + 2 * static_cast<int64_t>(sms) * (few ? TOK_ROWS : CV_ROWS) * a->head_dim);
   p.rows = a->n_rows;
   p.batch = a->batch;
   p.Hq = a->n_q_heads;
@@ -243,9 +280,9 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
   p.err = DevErr{nullptr, 1000000000ull};
   switch (a->head_dim) {
-    case 64: return launch_token<64>(p, sms, cuda_stream);
-    case 128: return launch_token<128>(p, sms, cuda_stream);
-    default: return launch_token<176>(p, sms, cuda_stream);
+    case 64: return few ? launch_token<64>(p, sms, cuda_stream) : launch_canvas<64>(cp, sms, cuda_stream);
+    case 128: return few ? launch_token<128>(p, sms, cuda_stream) : launch_canvas<128>(cp, sms, cuda_stream);
+    default: return few ? launch_token<176>(p, sms, cuda_stream) : launch_canvas<176>(cp, sms, cuda_stream);
   }
 }
 

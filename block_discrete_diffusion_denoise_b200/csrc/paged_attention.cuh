@@ -39,7 +39,7 @@ struct PagedAttnParams {
 };
 
 struct PagedRequest {
-  int t0, n, kv, nb, tiles;    // first row, rows, keys, key blocks of a tile, row tiles
+  int t0, n, kv, tiles;        // first row, rows, keys, row tiles
 };
 
 template <int ROWS>
@@ -48,9 +48,27 @@ __device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams& p, 
   r.t0 = min(max(p.cu_rows[b], 0), p.rows);
   r.n = max(min(p.cu_rows[b + 1], p.rows) - r.t0, 0);
   r.kv = min(max(p.kv_lens[b], 0), p.width << p.page_shift);
-  r.nb = r.kv > 0 ? (r.kv - 1) / PG_BK + 1 : 1;   // a tile without keys still writes its rows
   r.tiles = (r.n * (p.Hq / p.Hkv) + ROWS - 1) / ROWS;
   return r;
+}
+
+// key blocks that row tile t has to look at: up to the last key that its last row sees
+template <int ROWS>
+__device__ __forceinline__ int paged_blocks(const PagedAttnParams& p, const PagedRequest& r, int t) {
+  int keys = r.kv;
+  if (p.causal && t + 1 < r.tiles)
+    keys = min(keys, r.kv - r.n + ((t + 1) * ROWS - 1) / (p.Hq / p.Hkv) + 1);
+  return keys > 0 ? (keys - 1) / PG_BK + 1 : 1;   // a tile without keys still writes its rows
+}
+
+// units of a request
+template <int ROWS>
+__device__ __forceinline__ long long paged_units(const PagedAttnParams& p, const PagedRequest& r) {
+  if (r.tiles == 0) return 0;
+  if (!p.causal) return static_cast<long long>(r.tiles) * p.Hkv * paged_blocks<ROWS>(p, r, 0);
+  long long u = 0;
+  for (int t = 0; t < r.tiles; ++t) u += paged_blocks<ROWS>(p, r, t);
+  return u * p.Hkv;
 }
 
 // a CTA's stretch [lo, hi) of the line's `total` units, and where it starts:
@@ -72,10 +90,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int 
   const int per = (p.batch + blockDim.x - 1) / blockDim.x;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) {
-    const PagedRequest r = paged_request<ROWS>(p, b);
-    sum += static_cast<long long>(r.tiles) * p.Hkv * r.nb;
-  }
+  for (int b = b0; b < b1; ++b) sum += paged_units<ROWS>(p, paged_request<ROWS>(p, b));
   long long upto = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -97,8 +112,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int 
   long long at = before + upto - sum;
   if (g.lo < g.hi && g.lo >= at && g.lo < at + sum) {
     for (int b = b0; b < b1; ++b) {
-      const PagedRequest r = paged_request<ROWS>(p, b);
-      const long long u = static_cast<long long>(r.tiles) * p.Hkv * r.nb;
+      const long long u = paged_units<ROWS>(p, paged_request<ROWS>(p, b));
       if (g.lo < at + u) {
         found_b = b;
         found_rem = g.lo - at;
@@ -113,25 +127,36 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int 
   return g;
 }
 
-// Walks the tiles of a stretch: the key blocks [kb0, kb1) of row tile `tile`
-// of kv head h of request b.
+// Walks the tiles of a stretch: the key blocks [kb0, kb1) of the nb of row
+// tile `tile` of kv head h of request b.
 template <int ROWS>
 struct PagedWalk {
   PagedRequest r;
   int64_t left;
-  int b, tile, h, kb0, kb1;
+  int b, tile, h, nb, kb0, kb1;
 
   __device__ __forceinline__ PagedWalk(const PagedAttnParams& p, const PagedRange& g) : left(g.hi - g.lo), b(g.b) {
     if (left <= 0) return;
     r = paged_request<ROWS>(p, b);
-    const int64_t t = g.rem / r.nb;
-    tile = static_cast<int>(t / p.Hkv);
-    h = static_cast<int>(t % p.Hkv);
-    kb0 = static_cast<int>(g.rem % r.nb);
-    kb1 = static_cast<int>(min64(r.nb, kb0 + left));
+    tile = 0;
+    nb = paged_blocks<ROWS>(p, r, 0);
+    int64_t rem = g.rem;
+    if (!p.causal) {
+      const int64_t per_tile = static_cast<int64_t>(nb) * p.Hkv;
+      tile = static_cast<int>(rem / per_tile);
+      rem %= per_tile;
+    } else {
+      while (rem >= static_cast<int64_t>(nb) * p.Hkv && tile + 1 < r.tiles) {
+        rem -= static_cast<int64_t>(nb) * p.Hkv;
+        nb = paged_blocks<ROWS>(p, r, ++tile);
+      }
+    }
+    h = static_cast<int>(rem / nb);
+    kb0 = static_cast<int>(rem % nb);
+    kb1 = static_cast<int>(min64(nb, kb0 + left));
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
-  __device__ __forceinline__ bool whole() const { return kb0 == 0 && kb1 == r.nb; }
+  __device__ __forceinline__ bool whole() const { return kb0 == 0 && kb1 == nb; }
   __device__ __forceinline__ void next(const PagedAttnParams& p) {
     left -= kb1 - kb0;
     if (left <= 0) return;
@@ -148,10 +173,18 @@ struct PagedWalk {
           r = paged_request<ROWS>(p, b);
         } while (r.tiles == 0);
       }
+      nb = paged_blocks<ROWS>(p, r, tile);
     }
-    kb1 = static_cast<int>(min64(r.nb, left));
+    kb1 = static_cast<int>(min64(nb, left));
   }
 };
+
+// where column c of row r of a partial slot lies: rows of floats, or for the
+// 256-row tiles (a thread per row) columns of float4
+template <int ROWS, int D>
+__device__ __forceinline__ int64_t paged_part_at(int64_t slot, int r, int c) {
+  return ROWS == 16 ? (slot * ROWS + r) * D + c : ((slot * (D / 4) + c / 4) * ROWS + r) * 4 + c % 4;
+}
 
 // untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
@@ -247,9 +280,9 @@ __device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
         p.o[out * D + i % D] = 0x7fc0;
         if (p.lse) p.lse[out] = NAN;
       } else {
-        const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0)) * ROWS + i / D;
-        p.part[slot * D + i % D] = NAN;
-        p.part_ml[slot] = make_float2(0.f, NAN);
+        const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0);
+        p.part[paged_part_at<ROWS, D>(slot, i / D, i % D)] = NAN;
+        p.part_ml[slot * ROWS + i / D] = make_float2(0.f, NAN);
       }
     }
   }
@@ -495,7 +528,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       if (lane == 0) mbar_arrive(o_full);
       ok = __all_sync(0xffffffffu, mbar_wait(o_full, seg & 1, p.err) && !*abort_flag);
       if (!ok) break;
-      const int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (d.flags & TOK_SLOT1 ? 1 : 0)) * TOK_ROWS;
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (d.flags & TOK_SLOT1 ? 1 : 0);
       for (int i = threadIdx.x - 32; i < live * (D / 4); i += 32 * TOK_WARPS) {
         const int r = i / (D / 4), c4 = i % (D / 4) * 4;
         float M = -INFINITY;
@@ -522,8 +555,8 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
               make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
           if (p.lse && c4 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
         } else {
-          *reinterpret_cast<float4*>(p.part + (slot + r) * D + c4) = a;
-          if (c4 == 0) p.part_ml[slot + r] = make_float2(M, L);
+          *reinterpret_cast<float4*>(p.part + paged_part_at<TOK_ROWS, D>(slot, r, c4)) = a;
+          if (c4 == 0) p.part_ml[slot * TOK_ROWS + r] = make_float2(M, L);
         }
       }
       __syncwarp();
@@ -555,24 +588,26 @@ __global__ void __launch_bounds__(PG_MERGE_THREADS) paged_merge_kernel(const __g
     w.next(p);
     ++seg;
   }
-  const bool cut = w.more() && w.kb0 == 0 && w.kb1 < w.r.nb;   // the stretch's last tile goes on behind it
+  const bool cut = w.more() && w.kb0 == 0 && w.kb1 < w.nb;   // the stretch's last tile goes on behind it
   pdl_wait();
   if (!cut) return;
   const int live = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
-  const int64_t end = g.hi - w.kb1 + w.r.nb;                    // the tile's end on the line
+  const int64_t end = g.hi - w.kb1 + w.nb;                      // the tile's end on the line
   // the pieces behind this CTA's are the first of each stretch up to the one that holds unit end - 1
   // (floor(W c / N) <= u is c <= ((u + 1) N - 1) / W)
   const int last = static_cast<int>((end * g.ctas - 1) / g.total);
-  for (int i = threadIdx.x; i < live * (D / 4); i += PG_MERGE_THREADS) {
-    const int r = i / (D / 4), c4 = i % (D / 4) * 4;
-    int64_t slot = (static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0)) * ROWS + r;
-    float2 ml = p.part_ml[slot];
-    float4 a = *reinterpret_cast<const float4*>(p.part + slot * D + c4);
+  const int64_t slot0 = static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0);
+  for (int i = blockIdx.y * PG_MERGE_THREADS + threadIdx.x; i < ROWS * (D / 4); i += gridDim.y * PG_MERGE_THREADS) {
+    const int r = ROWS == 16 ? i / (D / 4) : i % ROWS, c4 = (ROWS == 16 ? i % (D / 4) : i / ROWS) * 4;
+    if (r >= live) continue;
+    float2 ml = p.part_ml[slot0 * ROWS + r];
+    float4 a = *reinterpret_cast<const float4*>(p.part + paged_part_at<ROWS, D>(slot0, r, c4));
     float M = ml.x, L = ml.y;
+#pragma unroll 4
     for (int x = blockIdx.x + 1; x <= last; ++x) {
-      slot = static_cast<int64_t>(x) * 2 * ROWS + r;
-      ml = p.part_ml[slot];
-      const float4 v = *reinterpret_cast<const float4*>(p.part + slot * D + c4);
+      const int64_t slot = static_cast<int64_t>(x) * 2;
+      ml = p.part_ml[slot * ROWS + r];
+      const float4 v = *reinterpret_cast<const float4*>(p.part + paged_part_at<ROWS, D>(slot, r, c4));
       const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
       const float e0 = ex2_approx(M - base), e1 = ex2_approx(ml.x - base);
       L = L * e0 + ml.y * e1;
