@@ -9,8 +9,8 @@
 //   S_0(j) PV_0(j-1) S_1(j) PV_1(j-1) S_0(j+1) ...
 // so that a tile's softmax has the other tile's products and its own next
 // scores to hide behind.  The warps are a persistent pipeline over the CTA's
-// stretch of units (paged_attention.cuh): a descriptor per unit, in a ring of
-// its own, tells the MMA and softmax warps what the producers fetched.
+// stretch of units (paged_attention.cuh); each role walks it by itself, and a
+// word per unit tells the softmax warps which keys the producers found.
 #pragma once
 
 #include "paged_attention.cuh"
@@ -19,7 +19,7 @@ namespace dg {
 
 constexpr int CV_TILE = 128;             // packed rows of a query tile (MMA M)
 constexpr int CV_ROWS = 2 * CV_TILE;
-constexpr int CV_DESCS = 8;
+constexpr int CV_MASKS = 8;               // ring of key masks, deeper than any role runs ahead
 constexpr int CV_SOFTMAX_WARP = 3;       // warps 0 K and Q, 1 V, 2 MMA, 3..6 and 7..10 softmax of tiles 0 and 1
 constexpr int CV_THREADS = 32 * (CV_SOFTMAX_WARP + 8);
 constexpr float CV_RESCALE_LOG2 = 8.f;
@@ -47,14 +47,52 @@ struct CanvasParams {
   CUtensorMap q_map;           // 4-D (D, G, Hkv, rows) over q; box (64, G, 1, 128 / G)
 };
 
-// what the MMA and softmax warps need to know of a unit
-struct CvDesc {
-  uint64_t valid;              // keys of the block in pages of the pool, below kv
-  int flags, nq;               // query tiles with live rows
-  int t0, n, kv, h;
-  int row0;                    // first packed row of the tile
-  int key0;                    // first key of the block
+// Matrix descriptors of one operand that differ in their start address only:
+// the low word carries it (16-byte units), the high word is the layout.
+struct UmmaOperand {
+  uint32_t lo, hi;
+  __device__ __forceinline__ explicit UmmaOperand(uint64_t d)
+      : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
 };
+
+// D[tmem] (+)= A B^T with the operands' start addresses moved by a_off and b_off bytes
+template <bool ACC>
+__device__ __forceinline__ void umma_at(uint32_t tmem_d, const UmmaOperand& a, uint32_t a_off, const UmmaOperand& b,
+                                        uint32_t b_off, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %2};\n\t"
+      "mov.b64 db, {%3, %4};\n\t"
+      "setp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(tmem_d),
+      "r"(a.lo + (a_off >> 4)), "r"(a.hi), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "n"(ACC ? 1 : 0)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+  uint64_t v;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi));
+  return v;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t f32x2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// two floats to bf16, nearest even, lo in the low half
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
 
 template <int D>
 __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __grid_constant__ CanvasParams cp) {
@@ -70,19 +108,18 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   uint64_t* k_empty = k_full + C::STAGES;
   uint64_t* v_full = k_empty + C::STAGES;
   uint64_t* v_empty = v_full + C::STAGES;
-  uint64_t* d_full = v_empty + C::STAGES;      // [CV_DESCS] K producer -> MMA and softmax: descriptor written
-  uint64_t* d_empty = d_full + CV_DESCS;       // [CV_DESCS] ... and read
-  uint64_t* s_full = d_empty + CV_DESCS;       // [2] MMA -> softmax q: scores ready
+  uint64_t* m_full = v_empty + C::STAGES;      // [CV_MASKS] K producer -> softmax: key mask written
+  uint64_t* s_full = m_full + CV_MASKS;        // [2] MMA -> softmax q: scores ready
   uint64_t* s_free = s_full + 2;               // [2] softmax q -> MMA: scores in registers
   uint64_t* p_full = s_free + 2;               // [2] softmax q -> MMA: P_q written
   uint64_t* o_done = p_full + 2;               // [2] MMA -> softmax q: O_q += P_q V complete
   uint64_t* o_free = o_done + 2;               // [2] softmax q -> MMA: O_q read at a tile's end
   uint64_t* drain = o_free + 2;
-  CvDesc* desc = reinterpret_cast<CvDesc*>(tail + 512);
+  uint64_t* key_mask = reinterpret_cast<uint64_t*>(tail + 512);  // [CV_MASKS] keys of the unit that exist
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail + 960);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 964);
-  static_assert((2 + 4 * C::STAGES + 2 * CV_DESCS + 11) * 8 <= 512, "tail layout");
-  static_assert(CV_DESCS * sizeof(CvDesc) <= 448, "tail layout");
+  static_assert((2 + 4 * C::STAGES + CV_MASKS + 11) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
+  static_assert(CV_MASKS >= C::STAGES + 4, "a mask is read before its slot comes round");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -97,10 +134,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 1);
     }
-    for (int s = 0; s < CV_DESCS; ++s) {
-      mbar_init(&d_full[s], 1);
-      mbar_init(&d_empty[s], 9);               // the MMA thread and eight softmax warps
-    }
+    for (int s = 0; s < CV_MASKS; ++s) mbar_init(&m_full[s], 1);
     for (int q = 0; q < 2; ++q) {
       mbar_init(&s_full[q], 1);
       mbar_init(&s_free[q], CV_TILE);
@@ -165,9 +199,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
         const int key = kb * PG_BK + my_piece * box;
         const bool good = page >= 0 && page < p.n_pages && key < w.r.kv;
         const uint32_t pmask = __ballot_sync(0xffffffffu, good && lane < pieces);
-        ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err) &&
-                                         (!is_k || mbar_wait(&d_empty[it % CV_DESCS], ((it / CV_DESCS) & 1) ^ 1, p.err)) &&
-                                         !*abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err) && !*abort_flag);
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&full[s], __popc(pmask) * box * 128 * C::DK);
@@ -177,19 +209,10 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
               if (pmask >> i & 1) valid |= (box == 64 ? ~uint64_t(0) : ((uint64_t(1) << box) - 1)) << (i * box);
             const int keys = w.r.kv - kb * PG_BK;
             if (keys < PG_BK) valid &= keys > 0 ? (uint64_t(1) << keys) - 1 : 0;
-            CvDesc d;
-            d.valid = valid;
-            d.flags = (kb == w.kb0 ? TOK_FIRST : 0) | (kb + 1 == w.kb1 ? TOK_LAST : 0) | (w.whole() ? TOK_WHOLE : 0) |
-                      (seg > 0 ? TOK_SLOT1 : 0);
-            d.nq = nq;
-            d.t0 = w.r.t0;
-            d.n = w.r.n;
-            d.kv = w.r.kv;
-            d.h = w.h;
-            d.row0 = row0;
-            d.key0 = kb * PG_BK;
-            desc[it % CV_DESCS] = d;
-            mbar_arrive(&d_full[it % CV_DESCS]);
+            // the slot's last reader has read it: this K slot came free STAGES units behind it, and the softmax of a
+            // tile is never more than two units behind its scores
+            key_mask[it % CV_MASKS] = valid;
+            mbar_arrive(&m_full[it % CV_MASKS]);
           }
         }
         __syncwarp();
@@ -198,13 +221,6 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
                       page * rows_per_page + (w.h << p.page_shift) + (key & ((1 << p.page_shift) - 1)), pol);
         issued |= 1u << s;
         par = (par & ~(1u << s)) | (((it / C::STAGES) & 1) << s);
-      }
-    }
-    if (is_k && ok && lane == 0) {
-      ok = mbar_wait(&d_empty[it % CV_DESCS], ((it / CV_DESCS) & 1) ^ 1, p.err);
-      if (ok) {
-        desc[it % CV_DESCS].flags = TOK_EXIT;
-        mbar_arrive(&d_full[it % CV_DESCS]);
       }
     }
     if (!ok) *abort_flag = 1;
@@ -219,62 +235,72 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     if (lane == 0) {
       constexpr uint32_t IDESC_S = umma_idesc_bf16(CV_TILE, PG_BK);             // Q, K both K-major
       constexpr uint32_t IDESC_PV = umma_idesc_bf16(CV_TILE, D) | (1u << 16);   // V is MN-major
-      const uint32_t q_addr = smem_u32(smem), k_addr = q_addr + C::K_OFF, v_addr = q_addr + C::V_OFF,
-                     p_addr = q_addr + C::P_OFF;
-      int cs[2] = {0, 0}, cpv[2] = {0, 0};     // score and P V products of each tile so far
-      int used[2] = {0, 0};                    // tiles that have held O_q
-      int seg = 0;
-      // O_q += P_q V of unit j (acc: not the tile's first)
-      auto pv = [&](int q, int j, bool acc) {
-        if (!mbar_wait(&p_full[q], cpv[q] & 1, p.err)) return false;
-        if (!acc && used[q] > 0 && !mbar_wait(&o_free[q], (used[q] - 1) & 1, p.err)) return false;
-        if (!acc) ++used[q];
+      const uint32_t at = smem_u32(smem);
+      const UmmaOperand q_op(umma_desc_sw128(at)), k_op(umma_desc_sw128(at + C::K_OFF));
+      const UmmaOperand p_op(umma_desc_sw128(at + C::P_OFF)), v_op(umma_desc_sw128_mn(at + C::V_OFF, PG_BK * 128));
+      int n0 = 0, n1 = 0;                      // products of tile 0 and of tile 1 so far (scores; P V one behind)
+      int held0 = 0, held1 = 0;                // row tiles that have used O_0, O_1
+      // S_q = Q_q K^T of unit j; n: the tile's number of them so far
+      auto scores = [&](int q, int j, int n) {
+        if (n > 0 && !mbar_wait(&s_free[q], (n - 1) & 1, p.err)) return false;
         tc_fence_after();
-        const uint32_t vb = v_addr + (j % C::STAGES) * C::KV_BYTES, pb = p_addr + q * C::P_BYTES;
+        UmmaOperand a = q_op, b = k_op;
+        a.lo += (q * C::Q_BYTES) >> 4;
+        b.lo += ((j % C::STAGES) * C::KV_BYTES) >> 4;
+        const uint32_t d = tmem_base + C::S_COL + q * PG_BK;
+        umma_at<false>(d, a, 0, b, 0, IDESC_S);
 #pragma unroll
-        for (int kk = 0; kk < PG_BK / 16; ++kk)
-          umma_bf16(tmem_base + C::O_COL + q * D, umma_desc_sw128(pb + kk * 32),
-                    umma_desc_sw128_mn(vb + kk * 2048, PG_BK * 128), IDESC_PV, (acc || kk > 0) ? 1u : 0u);
-        umma_commit(&o_done[q]);
-        ++cpv[q];
+        for (int kk = 1; kk < D / 16; ++kk)
+          umma_at<true>(d, a, (kk >> 2) * (CV_TILE * 128) + (kk & 3) * 32, b, (kk >> 2) * (PG_BK * 128) + (kk & 3) * 32,
+                        IDESC_S);
+        umma_commit(&s_full[q]);
         return true;
       };
-      bool prev_first = false;
-      for (int j = 0; ok; ++j) {
-        const int ds = j % CV_DESCS, ks = j % C::STAGES;
-        ok = mbar_wait(&d_full[ds], (j / CV_DESCS) & 1, p.err) && !*abort_flag;
-        if (!ok) break;
-        const int flags = desc[ds].flags, nq = desc[ds].nq;
-        if (flags & TOK_EXIT) break;
-        mbar_arrive(&d_empty[ds]);
-        const bool first = flags & TOK_FIRST;
-        ok = (!first || mbar_wait(q_full, seg & 1, p.err)) && mbar_wait(&k_full[ks], (j / C::STAGES) & 1, p.err);
-        for (int q = 0; q < nq && ok; ++q) {
-          if (cs[q] > 0) ok = mbar_wait(&s_free[q], (cs[q] - 1) & 1, p.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint32_t kb = k_addr + ks * C::KV_BYTES, qb = q_addr + q * C::Q_BYTES;
+      // O_q (+)= P_q V of unit j, the tile's n-th; first: the row tile's first unit, behind `held` others
+      auto outputs = [&](int q, int j, int n, bool first, int held) {
+        if (!mbar_wait(&p_full[q], n & 1, p.err)) return false;
+        if (first && held > 0 && !mbar_wait(&o_free[q], (held - 1) & 1, p.err)) return false;
+        tc_fence_after();
+        UmmaOperand a = p_op, b = v_op;
+        a.lo += (q * C::P_BYTES) >> 4;
+        b.lo += ((j % C::STAGES) * C::KV_BYTES) >> 4;
+        const uint32_t d = tmem_base + C::O_COL + q * D;
+        if (first)
+          umma_at<false>(d, a, 0, b, 0, IDESC_PV);
+        else
+          umma_at<true>(d, a, 0, b, 0, IDESC_PV);
 #pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk)
-            umma_bf16(tmem_base + C::S_COL + q * PG_BK, umma_desc_sw128(qb + (kk >> 2) * (CV_TILE * 128) + (kk & 3) * 32),
-                      umma_desc_sw128(kb + (kk >> 2) * (PG_BK * 128) + (kk & 3) * 32), IDESC_S, kk > 0 ? 1u : 0u);
-          umma_commit(&s_full[q]);
-          ++cs[q];
-          if (q == nq - 1) umma_commit(&k_empty[ks]);
-          if (!first) {
-            if (q == 0) ok = mbar_wait(&v_full[(j - 1) % C::STAGES], ((j - 1) / C::STAGES) & 1, p.err);
-            ok = ok && pv(q, j - 1, !prev_first);
-            if (ok && q == nq - 1) umma_commit(&v_empty[(j - 1) % C::STAGES]);
+        for (int kk = 1; kk < PG_BK / 16; ++kk) umma_at<true>(d, a, kk * 32, b, kk * 2048, IDESC_PV);
+        umma_commit(&o_done[q]);
+        return true;
+      };
+      int j = 0, seg = 0;
+      for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+        const bool two = w.r.n * G - w.tile * CV_ROWS > CV_TILE;
+        const int units = w.kb1 - w.kb0;
+        ok = mbar_wait(q_full, seg & 1, p.err);
+        // unit u's scores, then the products of unit u - 1
+        for (int u = 0; ok && u <= units; ++u, ++j) {
+          const int ks = j % C::STAGES, vs = (j + C::STAGES - 1) % C::STAGES;
+          const bool has_s = u < units, has_o = u > 0;
+          if (has_s) ok = !*abort_flag && mbar_wait(&k_full[ks], (j / C::STAGES) & 1, p.err) && scores(0, j, n0++);
+          if (ok && has_s && !two) umma_commit(&k_empty[ks]);
+          if (ok && has_o)
+            ok = mbar_wait(&v_full[vs], ((j - 1) / C::STAGES) & 1, p.err) &&
+                 outputs(0, j - 1, n0 - 1 - has_s, u == 1, held0);
+          if (two) {
+            if (ok && has_s) {
+              ok = scores(1, j, n1++);
+              if (ok) umma_commit(&k_empty[ks]);
+            }
+            if (ok && has_o) ok = outputs(1, j - 1, n1 - 1 - has_s, u == 1, held1);
           }
+          if (ok && has_o) umma_commit(&v_empty[vs]);
+          if (ok && u == units - 1) umma_commit(q_empty);
         }
-        if (ok && (flags & TOK_LAST)) {
-          umma_commit(q_empty);
-          ok = mbar_wait(&v_full[ks], (j / C::STAGES) & 1, p.err);
-          for (int q = 0; q < nq && ok; ++q) ok = pv(q, j, !first);
-          if (ok) umma_commit(&v_empty[ks]);
-          ++seg;
-        }
-        prev_first = first;
+        --j;
+        ++held0;
+        held1 += two;
       }
       if (!ok) *abort_flag = 1;
       // every MMA issued has completed before TMEM or its operands are released
@@ -289,111 +315,110 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     const uint32_t t_row = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t s_col = t_row + C::S_COL + wg * PG_BK, o_col = t_row + C::O_COL + wg * D;
     uint8_t* pdst = smem + C::P_OFF + wg * C::P_BYTES + rloc * 128;
-    float mref = -INFINITY, lsum = 0.f;
-    int lim = 0;                                     // keys [0, lim) are this row's
-    int n_s = 0;                                     // score tiles read so far
-    for (int j = 0;; ++j) {
-      const int ds = j % CV_DESCS;
-      // warp-uniform decisions: tcgen05.ld below is a warp-collective
-      ok = __all_sync(0xffffffffu, mbar_wait(&d_full[ds], (j / CV_DESCS) & 1, p.err) && !*abort_flag);
-      if (!ok) break;
-      const CvDesc d = desc[ds];
-      if (d.flags & TOK_EXIT) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&d_empty[ds]);
-      if (wg >= d.nq) continue;
-      const int r = d.row0 + wg * CV_TILE + rloc;    // packed row of the request
-      const bool live = r < d.n * G;
-      const bool first = d.flags & TOK_FIRST;
-      if (first) {
-        mref = -INFINITY;
-        lsum = 0.f;
-        lim = !live ? 0 : p.causal ? min(d.kv, d.kv - d.n + r / G + 1) : d.kv;
+    int j = 0, seg = 0, n_s = 0;                     // units of the stretch, tiles, score tiles read so far
+    for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+      const int row0 = w.tile * CV_ROWS, units = w.kb1 - w.kb0;
+      if (w.r.n * G - row0 <= wg * CV_TILE) {        // no live row in this tile
+        j += units;
+        continue;
       }
-      ok = __all_sync(0xffffffffu, mbar_wait(&s_full[wg], n_s & 1, p.err) && !*abort_flag);
-      if (!ok) break;
-      tc_fence_after();
-      float s[64];
-      tmem_ld64(s_col, s);
-      tc_fence_before();
-      mbar_arrive(&s_free[wg]);
-      const bool full = __all_sync(0xffffffffu, !live || lim - d.key0 >= PG_BK) && d.valid == ~uint64_t(0);
-      if (!full) {
-        const int lj = lim - d.key0;
-#pragma unroll
-        for (int c = 0; c < PG_BK; ++c)
-          if (c >= lj || !(d.valid >> c & 1)) s[c] = -INFINITY;
-      }
-      float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < PG_BK; ++c) mx[c & 3] = fmaxf(mx[c & 3], s[c]);
-      // scale > 0, so the maximum of the scaled scores is the scaled maximum
-      const float mblk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
-      // P = 2^(s - mref); the reference is raised only when a block passes it by 2^8, so that rescaling O is rare
-      const bool resc = mblk > mref + CV_RESCALE_LOG2;          // false while nothing is visible
-      const float factor = resc ? ex2_approx(mref - mblk) : 1.f;  // 0 when mref = -inf
-      if (resc) mref = mblk;
-      const float base = mref == -INFINITY ? 0.f : mref;
-      lsum *= factor;
-      float l = 0.f;
-      uint32_t pk[PG_BK / 2];
-#pragma unroll
-      for (int c = 0; c < PG_BK / 2; ++c) {
-        // p enters the second product in bf16 (2^-9 of each, averaging out over keys); its sum stays fp32
-        const float p0 = ex2_approx(fmaf(s[2 * c], p.scale_log2, -base));
-        const float p1 = ex2_approx(fmaf(s[2 * c + 1], p.scale_log2, -base));
-        l += p0 + p1;
-        pk[c] = pack_bf16x2(p0, p1);
-      }
-      lsum += l;
-      if (!first) {
-        // O_q += P_q V of the unit before has completed: O_q is stable and P_q's buffer free
-        ok = __all_sync(0xffffffffu, mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err));
+      const int r = row0 + wg * CV_TILE + rloc;      // packed row of the request
+      const bool live = r < w.r.n * G;
+      // keys [0, lim) are this row's
+      const int lim = !live ? 0 : p.causal ? min(w.r.kv, w.r.kv - w.r.n + r / G + 1) : w.r.kv;
+      const int lim_all = __reduce_min_sync(0xffffffffu, live ? lim : INT32_MAX);
+      float mref = -INFINITY, lsum = 0.f;
+      for (int u = 0; u < units; ++u, ++j, ++n_s) {
+        const int key0 = (w.kb0 + u) * PG_BK;
+        // warp-uniform decisions: tcgen05.ld below is a warp-collective
+        ok = __all_sync(0xffffffffu, mbar_wait(&m_full[j % CV_MASKS], (j / CV_MASKS) & 1, p.err));
+        const uint64_t valid = key_mask[j % CV_MASKS];
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[wg], n_s & 1, p.err) && !*abort_flag);
         if (!ok) break;
         tc_fence_after();
-        if (__any_sync(0xffffffffu, resc)) {
-#pragma unroll 1
-          for (int c0 = 0; c0 < D; c0 += 16) {
-            float v[16];
-            tmem_ld16(o_col + c0, v);
+        float s[PG_BK];
+        tmem_ld64(s_col, s);
+        tc_fence_before();
+        mbar_arrive(&s_free[wg]);
+        if (key0 + PG_BK > lim_all || valid != ~uint64_t(0)) {
+          const int lj = lim - key0;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) v[e] *= factor;
-            tmem_st16(o_col + c0, v);
-          }
-          tmem_st_wait();
+          for (int c = 0; c < PG_BK; ++c)
+            if (c >= lj || !(valid >> c & 1)) s[c] = -INFINITY;
         }
-      }
-      if (d.valid != ~uint64_t(0)) {
-        // values of masked keys may be anything, and 0 * NaN is NaN: they are cleared (by both warpgroups, each
-        // before its own product) in the swizzled rows of the V block
-        ok = __all_sync(0xffffffffu, mbar_wait(&v_full[j % C::STAGES], (j / C::STAGES) & 1, p.err));
-        if (!ok) break;
-        uint8_t* vb = smem + C::V_OFF + (j % C::STAGES) * C::KV_BYTES;
-        for (int i = rloc; i < PG_BK * 8; i += CV_TILE)
-          if (!(d.valid >> (i / 8) & 1)) {
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int b = 0; b < C::DK; ++b) reinterpret_cast<uint4*>(vb + b * PG_BK * 128)[i] = make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < PG_BK; c += 2) mx[(c >> 1) & 3] = fmaxf(mx[(c >> 1) & 3], fmaxf(s[c], s[c + 1]));
+        // scale > 0, so the maximum of the scaled scores is the scaled maximum
+        const float mblk = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.scale_log2;
+        // P = 2^(s - mref); the reference is raised only when a block passes it by 2^8, so that rescaling O is rare
+        const bool resc = mblk > mref + CV_RESCALE_LOG2;          // false while nothing is visible
+        const float factor = resc ? ex2_approx(mref - mblk) : 1.f;  // 0 when mref = -inf
+        if (resc) mref = mblk;
+        const float base = mref == -INFINITY ? 0.f : mref;
+        const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2), base2 = f32x2(-base, -base);
+        uint64_t l2[2] = {0, 0};
+        uint32_t pk[PG_BK / 2];
+#pragma unroll
+        for (int c = 0; c < PG_BK / 2; ++c) {
+          // p enters the second product in bf16 (2^-9 of each, averaging out over keys); its sum stays fp32
+          float x0, x1;
+          f32x2_split(f32x2_fma(f32x2(s[2 * c], s[2 * c + 1]), scale2, base2), x0, x1);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          l2[c & 1] = f32x2_add(l2[c & 1], f32x2(p0, p1));
+          pk[c] = cvt_bf16x2(p0, p1);
+        }
+        float l0, l1;
+        f32x2_split(f32x2_add(l2[0], l2[1]), l0, l1);
+        lsum = lsum * factor + (l0 + l1);
+        if (u > 0) {
+          // O_q += P_q V of the unit before has completed: O_q is stable and P_q's buffer free
+          ok = __all_sync(0xffffffffu, mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err));
+          if (!ok) break;
+          tc_fence_after();
+          if (__any_sync(0xffffffffu, resc)) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < D; c0 += 16) {
+              float v[16];
+              tmem_ld16(o_col + c0, v);
+#pragma unroll
+              for (int e = 0; e < 16; ++e) v[e] *= factor;
+              tmem_st16(o_col + c0, v);
+            }
+            tmem_st_wait();
           }
-      }
-      // row rloc of a K-major 128-byte-swizzled tile: 16-byte chunk c lands at c ^ (row & 7)
+        }
+        if (valid != ~uint64_t(0)) {
+          // values of masked keys may be anything, and 0 * NaN is NaN: they are cleared (by both warpgroups, each
+          // before its own product) in the swizzled rows of the V block
+          ok = __all_sync(0xffffffffu, mbar_wait(&v_full[j % C::STAGES], (j / C::STAGES) & 1, p.err));
+          if (!ok) break;
+          uint8_t* vb = smem + C::V_OFF + (j % C::STAGES) * C::KV_BYTES;
+          for (int i = rloc; i < PG_BK * 8; i += CV_TILE)
+            if (!(valid >> (i / 8) & 1)) {
 #pragma unroll
-      for (int ch = 0; ch < 8; ++ch)
-        *reinterpret_cast<uint4*>(pdst + ((ch ^ (rloc & 7)) << 4)) =
-            make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
-      fence_proxy_async_smem();
-      tc_fence_before();
-      mbar_arrive(&p_full[wg]);
-      ++n_s;
-      if (!(d.flags & TOK_LAST)) continue;
+              for (int b = 0; b < C::DK; ++b) reinterpret_cast<uint4*>(vb + b * PG_BK * 128)[i] = make_uint4(0, 0, 0, 0);
+            }
+        }
+        // row rloc of a K-major 128-byte-swizzled tile: 16-byte chunk c lands at c ^ (row & 7)
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch)
+          *reinterpret_cast<uint4*>(pdst + ((ch ^ (rloc & 7)) << 4)) =
+              make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+        fence_proxy_async_smem();
+        tc_fence_before();
+        mbar_arrive(&p_full[wg]);
+      }
+      if (!ok) break;
 
       // ------------- the tile's end: its rows, or their partial slot -------------
       ok = __all_sync(0xffffffffu, mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err) && !*abort_flag);
       if (!ok) break;
       tc_fence_after();
-      const bool whole = d.flags & TOK_WHOLE;
+      const bool whole = w.whole();
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
-      const int64_t row = live ? paged_out_row(p, d.t0, r, d.h) : 0;
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (d.flags & TOK_SLOT1 ? 1 : 0);
+      const int64_t row = live ? paged_out_row(p, w.r.t0, r, w.h) : 0;
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0);
 #pragma unroll 1
       for (int c0 = 0; c0 < D; c0 += 16) {
         float v[16];
@@ -403,10 +428,10 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
           uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c0);
 #pragma unroll
           for (int e = 0; e < 16; ++e) v[e] *= inv;
-          dst[0] = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                              pack_bf16x2(v[6], v[7]));
-          dst[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
-                              pack_bf16x2(v[14], v[15]));
+          dst[0] = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
+                              cvt_bf16x2(v[6], v[7]));
+          dst[1] = make_uint4(cvt_bf16x2(v[8], v[9]), cvt_bf16x2(v[10], v[11]), cvt_bf16x2(v[12], v[13]),
+                              cvt_bf16x2(v[14], v[15]));
         } else {
 #pragma unroll
           for (int e = 0; e < 16; e += 4)
