@@ -47,6 +47,20 @@ struct CanvasParams {
   CUtensorMap q_map;           // 4-D (D, G, Hkv, rows) over q; box (64, G, 1, 128 / G)
 };
 
+// The whole MMA warp runs the issuing code, and one elected lane's
+// instructions take effect: descriptors and addresses then stay in uniform
+// registers, where tcgen05.mma wants them (a lane-0 branch took 65 cycles per
+// instruction to move them there, the products themselves 48 to 88).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is;
+}
+
 // Matrix descriptors of one operand that differ in their start address only:
 // the low word carries it (16-byte units), the high word is the layout.
 struct UmmaOperand {
@@ -57,16 +71,39 @@ struct UmmaOperand {
 
 // D[tmem] (+)= A B^T with the operands' start addresses moved by a_off and b_off bytes
 template <bool ACC>
-__device__ __forceinline__ void umma_at(uint32_t tmem_d, const UmmaOperand& a, uint32_t a_off, const UmmaOperand& b,
-                                        uint32_t b_off, uint32_t idesc) {
+__device__ __forceinline__ void umma_at(uint32_t lead, uint32_t tmem_d, const UmmaOperand& a, uint32_t a_off,
+                                        const UmmaOperand& b, uint32_t b_off, uint32_t idesc) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
       "mov.b64 da, {%1, %2};\n\t"
       "mov.b64 db, {%3, %4};\n\t"
       "setp.ne.b32 p, %6, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(tmem_d),
-      "r"(a.lo + (a_off >> 4)), "r"(a.hi), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "n"(ACC ? 1 : 0)
+      "setp.ne.b32 q, %7, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %5, p;\n\t}" ::"r"(tmem_d),
+      "r"(a.lo + (a_off >> 4)), "r"(a.hi), "r"(b.lo + (b_off >> 4)), "r"(b.hi), "r"(idesc), "n"(ACC ? 1 : 0), "r"(lead)
       : "memory");
+}
+
+__device__ __forceinline__ void umma_commit_lead(uint32_t lead, uint64_t* bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+      "r"(lead)
+      : "memory");
+}
+
+// mbar_wait by a whole warp with one answer
+__device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, const DevErr& err) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  const uint64_t t0 = globaltimer_ns();
+  while (true) {
+    if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > err.limit_ns)) {
+      raise_error(err, ERR_TIMEOUT);
+      return false;
+    }
+  }
 }
 
 __device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
@@ -232,81 +269,82 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     }
   } else if (warp == 2) {
     // -------------------------------- MMA issuer --------------------------------
-    if (lane == 0) {
-      constexpr uint32_t IDESC_S = umma_idesc_bf16(CV_TILE, PG_BK);             // Q, K both K-major
-      constexpr uint32_t IDESC_PV = umma_idesc_bf16(CV_TILE, D) | (1u << 16);   // V is MN-major
-      const uint32_t at = smem_u32(smem);
-      const UmmaOperand q_op(umma_desc_sw128(at)), k_op(umma_desc_sw128(at + C::K_OFF));
-      const UmmaOperand p_op(umma_desc_sw128(at + C::P_OFF)), v_op(umma_desc_sw128_mn(at + C::V_OFF, PG_BK * 128));
-      int n0 = 0, n1 = 0;                      // products of tile 0 and of tile 1 so far (scores; P V one behind)
-      int held0 = 0, held1 = 0;                // row tiles that have used O_0, O_1
-      // S_q = Q_q K^T of unit j; n: the tile's number of them so far
-      auto scores = [&](int q, int j, int n) {
-        if (n > 0 && !mbar_wait(&s_free[q], (n - 1) & 1, p.err)) return false;
-        tc_fence_after();
-        UmmaOperand a = q_op, b = k_op;
-        a.lo += (q * C::Q_BYTES) >> 4;
-        b.lo += ((j % C::STAGES) * C::KV_BYTES) >> 4;
-        const uint32_t d = tmem_base + C::S_COL + q * PG_BK;
-        umma_at<false>(d, a, 0, b, 0, IDESC_S);
+    constexpr uint32_t IDESC_S = umma_idesc_bf16(CV_TILE, PG_BK);             // Q, K both K-major
+    constexpr uint32_t IDESC_PV = umma_idesc_bf16(CV_TILE, D) | (1u << 16);   // V is MN-major
+    const uint32_t lead = elect_one();
+    const uint32_t at = smem_u32(smem), tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
+    const UmmaOperand q_op(umma_desc_sw128(at)), k_op(umma_desc_sw128(at + C::K_OFF));
+    const UmmaOperand p_op(umma_desc_sw128(at + C::P_OFF)), v_op(umma_desc_sw128_mn(at + C::V_OFF, PG_BK * 128));
+    int n0 = 0, n1 = 0;                      // scores of tile 0 and of tile 1 so far (P V is one behind)
+    int held0 = 0, held1 = 0;                // row tiles that have used O_0, O_1
+    // S_q = Q_q K^T of unit j; n: the tile's number of them so far
+    auto scores = [&](int q, int j, int n) {
+      if (n > 0 && !mbar_wait_warp(&s_free[q], (n - 1) & 1, p.err)) return false;
+      tc_fence_after();
+      UmmaOperand a = q_op, b = k_op;
+      a.lo += (q * C::Q_BYTES) >> 4;
+      b.lo += ((j % C::STAGES) * C::KV_BYTES) >> 4;
+      const uint32_t d = tmem + C::S_COL + q * PG_BK;
+      umma_at<false>(lead, d, a, 0, b, 0, IDESC_S);
 #pragma unroll
-        for (int kk = 1; kk < D / 16; ++kk)
-          umma_at<true>(d, a, (kk >> 2) * (CV_TILE * 128) + (kk & 3) * 32, b, (kk >> 2) * (PG_BK * 128) + (kk & 3) * 32,
-                        IDESC_S);
-        umma_commit(&s_full[q]);
-        return true;
-      };
-      // O_q (+)= P_q V of unit j, the tile's n-th; first: the row tile's first unit, behind `held` others
-      auto outputs = [&](int q, int j, int n, bool first, int held) {
-        if (!mbar_wait(&p_full[q], n & 1, p.err)) return false;
-        if (first && held > 0 && !mbar_wait(&o_free[q], (held - 1) & 1, p.err)) return false;
-        tc_fence_after();
-        UmmaOperand a = p_op, b = v_op;
-        a.lo += (q * C::P_BYTES) >> 4;
-        b.lo += ((j % C::STAGES) * C::KV_BYTES) >> 4;
-        const uint32_t d = tmem_base + C::O_COL + q * D;
-        if (first)
-          umma_at<false>(d, a, 0, b, 0, IDESC_PV);
-        else
-          umma_at<true>(d, a, 0, b, 0, IDESC_PV);
+      for (int kk = 1; kk < D / 16; ++kk)
+        umma_at<true>(lead, d, a, (kk >> 2) * (CV_TILE * 128) + (kk & 3) * 32, b,
+                      (kk >> 2) * (PG_BK * 128) + (kk & 3) * 32, IDESC_S);
+      umma_commit_lead(lead, &s_full[q]);
+      return true;
+    };
+    // O_q (+)= P_q V of unit j, the tile's n-th; first: the row tile's first unit, behind `held` others
+    auto outputs = [&](int q, int j, int n, bool first, int held) {
+      if (!mbar_wait_warp(&p_full[q], n & 1, p.err)) return false;
+      if (first && held > 0 && !mbar_wait_warp(&o_free[q], (held - 1) & 1, p.err)) return false;
+      tc_fence_after();
+      UmmaOperand a = p_op, b = v_op;
+      a.lo += (q * C::P_BYTES) >> 4;
+      b.lo += ((j % C::STAGES) * C::KV_BYTES) >> 4;
+      const uint32_t d = tmem + C::O_COL + q * D;
+      if (first)
+        umma_at<false>(lead, d, a, 0, b, 0, IDESC_PV);
+      else
+        umma_at<true>(lead, d, a, 0, b, 0, IDESC_PV);
 #pragma unroll
-        for (int kk = 1; kk < PG_BK / 16; ++kk) umma_at<true>(d, a, kk * 32, b, kk * 2048, IDESC_PV);
-        umma_commit(&o_done[q]);
-        return true;
-      };
-      int j = 0, seg = 0;
-      for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
-        const bool two = w.r.n * G - w.tile * CV_ROWS > CV_TILE;
-        const int units = w.kb1 - w.kb0;
-        ok = mbar_wait(q_full, seg & 1, p.err);
-        // unit u's scores, then the products of unit u - 1
-        for (int u = 0; ok && u <= units; ++u, ++j) {
-          const int ks = j % C::STAGES, vs = (j + C::STAGES - 1) % C::STAGES;
-          const bool has_s = u < units, has_o = u > 0;
-          if (has_s) ok = !*abort_flag && mbar_wait(&k_full[ks], (j / C::STAGES) & 1, p.err) && scores(0, j, n0++);
-          if (ok && has_s && !two) umma_commit(&k_empty[ks]);
-          if (ok && has_o)
-            ok = mbar_wait(&v_full[vs], ((j - 1) / C::STAGES) & 1, p.err) &&
-                 outputs(0, j - 1, n0 - 1 - has_s, u == 1, held0);
-          if (two) {
-            if (ok && has_s) {
-              ok = scores(1, j, n1++);
-              if (ok) umma_commit(&k_empty[ks]);
-            }
-            if (ok && has_o) ok = outputs(1, j - 1, n1 - 1 - has_s, u == 1, held1);
+      for (int kk = 1; kk < PG_BK / 16; ++kk) umma_at<true>(lead, d, a, kk * 32, b, kk * 2048, IDESC_PV);
+      umma_commit_lead(lead, &o_done[q]);
+      return true;
+    };
+    int j = 0, seg = 0;
+    for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+      const int two = __shfl_sync(0xffffffffu, w.r.n * G - w.tile * CV_ROWS > CV_TILE, 0);
+      const int units = __shfl_sync(0xffffffffu, w.kb1 - w.kb0, 0);
+      ok = mbar_wait_warp(q_full, seg & 1, p.err);
+      // unit u's scores, then the products of unit u - 1
+      for (int u = 0; ok && u <= units; ++u, ++j) {
+        const int ks = j % C::STAGES, vs = (j + C::STAGES - 1) % C::STAGES;
+        const bool has_s = u < units, has_o = u > 0;
+        if (has_s)
+          ok = __all_sync(0xffffffffu, !*abort_flag) && mbar_wait_warp(&k_full[ks], (j / C::STAGES) & 1, p.err) &&
+               scores(0, j, n0++);
+        if (ok && has_s && !two) umma_commit_lead(lead, &k_empty[ks]);
+        if (ok && has_o)
+          ok = mbar_wait_warp(&v_full[vs], ((j - 1) / C::STAGES) & 1, p.err) &&
+               outputs(0, j - 1, n0 - 1 - has_s, u == 1, held0);
+        if (two) {
+          if (ok && has_s) {
+            ok = scores(1, j, n1++);
+            if (ok) umma_commit_lead(lead, &k_empty[ks]);
           }
-          if (ok && has_o) umma_commit(&v_empty[vs]);
-          if (ok && u == units - 1) umma_commit(q_empty);
+          if (ok && has_o) ok = outputs(1, j - 1, n1 - 1 - has_s, u == 1, held1);
         }
-        --j;
-        ++held0;
-        held1 += two;
+        if (ok && has_o) umma_commit_lead(lead, &v_empty[vs]);
+        if (ok && u == units - 1) umma_commit_lead(lead, q_empty);
       }
-      if (!ok) *abort_flag = 1;
-      // every MMA issued has completed before TMEM or its operands are released
-      umma_commit(drain);
-      mbar_wait(drain, 0, p.err);
+      --j;
+      ++held0;
+      held1 += two;
     }
+    if (!ok) *abort_flag = 1;
+    // every MMA issued has completed before TMEM or its operands are released
+    umma_commit_lead(lead, drain);
+    mbar_wait_warp(drain, 0, p.err);
   } else {
     // ----------------------- softmax warpgroup of tile wg -----------------------
     const int wg = (warp - CV_SOFTMAX_WARP) >> 2;
