@@ -120,7 +120,7 @@ bool few_rows(const dg_paged_attention_args* a) {
 
 int64_t paged_workspace(const dg_paged_attention_args* a, int sms) {
   const int64_t rows = few_rows(a) ? TOK_ROWS : CV_ROWS;
-  return 2 * sms * rows * (a->head_dim * 4 + 8);
+  return 2 * sms * rows * (a->head_dim * 4 + 8) + sms * static_cast<int64_t>(sizeof(PagedCut));
 }
 
 // Queries [row][Hq][D] seen as (D, G, Hkv, row): a box of 64 columns x G heads
@@ -149,7 +149,7 @@ template <int D>
 dg_status launch_canvas(const CanvasParams& p, int sms, void* stream) {
   const dg_status st = paged_launch(paged_canvas_kernel<D>, dim3(sms), CV_THREADS, CvCfg<D>::SMEM, stream, p);
   if (st != DG_OK) return st;
-  return paged_launch(paged_merge_kernel<CV_ROWS, D>, dim3(sms, 8), PG_MERGE_THREADS, 0, stream, p.a, true);
+  return paged_launch(paged_merge_kernel<CV_ROWS, D>, dim3(sms, D / 16), PG_MERGE_THREADS, 0, stream, p.a, true);
 }
 
 }  // namespace
@@ -268,7 +268,9 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   p.o = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
   p.part = static_cast<float*>(a->workspace);
-  p.part_ml = reinterpret_cast<float2*>(p.part + 2 * static_cast<int64_t>(sms) * (few ? TOK_ROWS : CV_ROWS) * a->head_dim);
+  const int64_t part_rows = 2 * static_cast<int64_t>(sms) * (few ? TOK_ROWS : CV_ROWS);
+  p.part_ml = reinterpret_cast<float2*>(p.part + part_rows * a->head_dim);
+  p.cuts = reinterpret_cast<PagedCut*>(p.part_ml + part_rows);
   p.rows = a->n_rows;
   p.batch = a->batch;
   p.Hq = a->n_q_heads;

@@ -20,6 +20,15 @@ namespace dg {
 
 constexpr int PG_BK = 64;      // keys per unit
 
+// A tile that a CTA's stretch begins and the next ones finish; rows = 0: none.
+struct PagedCut {
+  int rows;                    // live packed rows of the tile
+  int t0, row0, h;             // the request's first row, the tile's first packed row, kv head
+  int slot;                    // partial slot of the first piece
+  int last;                    // CTA of the last piece (the others are slot 2 c of the CTAs up to it)
+  int pad[2];
+};
+
 struct PagedAttnParams {
   CUtensorMap k_map;           // 2-D (D, n_pages * Hkv * page_size) over the pool; box (64, min(page_size, 64))
   CUtensorMap v_map;
@@ -33,6 +42,7 @@ struct PagedAttnParams {
   float* lse;                  // [rows][Hq] or null
   float* part;                 // [CTA][2][tile rows][D] raw rows of cut tiles
   float2* part_ml;             // [CTA][2][tile rows] their (max in log2 units, sum)
+  PagedCut* cuts;              // [CTA]
   int rows, batch, Hq, Hkv, n_pages, page_shift, width, causal;
   float scale_log2;            // log2(e) * scale
   DevErr err;
@@ -186,6 +196,24 @@ __device__ __forceinline__ int64_t paged_part_at(int64_t slot, int r, int c) {
   return ROWS == 16 ? (slot * ROWS + r) * D + c : ((slot * (D / 4) + c / 4) * ROWS + r) * 4 + c % 4;
 }
 
+// the tile that is left unfinished at the end of tile number seg of a stretch
+template <int ROWS>
+__device__ __forceinline__ PagedCut paged_cut(const PagedAttnParams& p, const PagedRange& g, const PagedWalk<ROWS>& w,
+                                              int seg) {
+  PagedCut c{};
+  if (w.kb0 > 0 || w.kb1 == w.nb) return c;
+  c.rows = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
+  c.t0 = w.r.t0;
+  c.row0 = w.tile * ROWS;
+  c.h = w.h;
+  c.slot = 2 * blockIdx.x + (seg > 0);
+  // the pieces behind this one are the first of each stretch up to the one that holds the tile's last unit,
+  // end - 1: floor(W c / N) <= u is c <= ((u + 1) N - 1) / W
+  const int64_t end = g.hi + (w.nb - w.kb1);
+  c.last = static_cast<int>((end * g.ctas - 1) / g.total);
+  return c;
+}
+
 // untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -272,7 +300,9 @@ __device__ __forceinline__ int64_t paged_out_row(const PagedAttnParams& p, int t
 template <int ROWS, int D>
 __device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
   int seg = 0;
+  PagedCut cut{};
   for (PagedWalk<ROWS> w(p, g); w.more(); w.next(p), ++seg) {
+    cut = paged_cut<ROWS>(p, g, w, seg);
     const int live = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
     for (int i = threadIdx.x; i < live * D; i += blockDim.x) {
       const int64_t out = paged_out_row(p, w.r.t0, w.tile * ROWS + i / D, w.h);
@@ -286,6 +316,7 @@ __device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
       }
     }
   }
+  if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut;
 }
 
 template <int D>
@@ -337,7 +368,9 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     const uint64_t pol = policy_evict_first();
     int it = 0, seg = 0;
     uint32_t issued = 0, par = 0;
+    PagedCut cut{};
     for (PagedWalk<TOK_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+      cut = paged_cut<TOK_ROWS>(p, g, w, seg);
       const int32_t* tab = p.table + w.b * p.table_stride;
       const int live = min(w.r.n * G - w.tile * TOK_ROWS, TOK_ROWS);
       int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
@@ -394,6 +427,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       }
     }
     if (lane == 0) {
+      p.cuts[blockIdx.x] = cut;
       const int s = it % C::STAGES;
       if (ok && mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err)) {
         desc[s].flags = TOK_EXIT;
@@ -570,58 +604,55 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
 }
 
 // ----------------------------------------------------------------------------
-// Joins the tiles that the stretches cut.  CTA c takes the tile that starts
-// in stretch c and ends behind it, if there is one:
+// Joins the tiles that the stretches cut, from the attention kernel's list:
 //   o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i
-// over its pieces in key order.  Launched with the attention kernel still
-// running, so its own start and scan of the batch cost nothing.
+// over a tile's pieces in key order.  A thread takes COLS groups of four
+// columns of one row.  Launched while the attention kernel still runs.
 // ----------------------------------------------------------------------------
 constexpr int PG_MERGE_THREADS = 256;
+template <int ROWS>
+constexpr int paged_merge_cols() { return ROWS == 16 ? 1 : 4; }
 
 template <int ROWS, int D>
 __global__ void __launch_bounds__(PG_MERGE_THREADS) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
   DG_TIMELINE_SCOPE(TLK_ATTN_MERGE);
-  const PagedRange g = paged_range<ROWS>(p, blockIdx.x, gridDim.x);
-  PagedWalk<ROWS> w(p, g);
-  int seg = 0;
-  while (w.more() && w.left > w.kb1 - w.kb0) {
-    w.next(p);
-    ++seg;
-  }
-  const bool cut = w.more() && w.kb0 == 0 && w.kb1 < w.nb;   // the stretch's last tile goes on behind it
+  constexpr int COLS = paged_merge_cols<ROWS>(), GROUPS = D / 4 / COLS;
   pdl_wait();
-  if (!cut) return;
-  const int live = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
-  const int64_t end = g.hi - w.kb1 + w.nb;                      // the tile's end on the line
-  // the pieces behind this CTA's are the first of each stretch up to the one that holds unit end - 1
-  // (floor(W c / N) <= u is c <= ((u + 1) N - 1) / W)
-  const int last = static_cast<int>((end * g.ctas - 1) / g.total);
-  const int64_t slot0 = static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0);
-  for (int i = blockIdx.y * PG_MERGE_THREADS + threadIdx.x; i < ROWS * (D / 4); i += gridDim.y * PG_MERGE_THREADS) {
-    const int r = ROWS == 16 ? i / (D / 4) : i % ROWS, c4 = (ROWS == 16 ? i % (D / 4) : i / ROWS) * 4;
-    if (r >= live) continue;
-    float2 ml = p.part_ml[slot0 * ROWS + r];
-    float4 a = *reinterpret_cast<const float4*>(p.part + paged_part_at<ROWS, D>(slot0, r, c4));
-    float M = ml.x, L = ml.y;
+  const PagedCut cut = p.cuts[blockIdx.x];
+  for (int i = blockIdx.y * PG_MERGE_THREADS + threadIdx.x; i < ROWS * GROUPS; i += gridDim.y * PG_MERGE_THREADS) {
+    // neighbouring threads: columns of a row where the rows lie whole, else rows
+    const int r = ROWS == 16 ? i / GROUPS : i % ROWS, c0 = (ROWS == 16 ? i % GROUPS : i / ROWS) * COLS * 4;
+    if (r >= cut.rows) continue;
+    float M = p.part_ml[static_cast<int64_t>(cut.slot) * ROWS + r].x;
 #pragma unroll 4
-    for (int x = blockIdx.x + 1; x <= last; ++x) {
-      const int64_t slot = static_cast<int64_t>(x) * 2;
-      ml = p.part_ml[slot * ROWS + r];
-      const float4 v = *reinterpret_cast<const float4*>(p.part + paged_part_at<ROWS, D>(slot, r, c4));
-      const float mn = fmaxf(M, ml.x), base = mn == -INFINITY ? 0.f : mn;
-      const float e0 = ex2_approx(M - base), e1 = ex2_approx(ml.x - base);
-      L = L * e0 + ml.y * e1;
-      a.x = a.x * e0 + v.x * e1;
-      a.y = a.y * e0 + v.y * e1;
-      a.z = a.z * e0 + v.z * e1;
-      a.w = a.w * e0 + v.w * e1;
-      M = mn;
+    for (int x = blockIdx.x + 1; x <= cut.last; ++x) M = fmaxf(M, p.part_ml[static_cast<int64_t>(2 * x) * ROWS + r].x);
+    const float base = M == -INFINITY ? 0.f : M;
+    float L = 0.f;
+    float4 a[COLS];
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int x = blockIdx.x; x <= cut.last; ++x) {
+      const int64_t slot = x == blockIdx.x ? cut.slot : 2 * x;
+      const float2 ml = p.part_ml[slot * ROWS + r];
+      const float e = ex2_approx(ml.x - base);
+      L += e * ml.y;
+#pragma unroll
+      for (int k = 0; k < COLS; ++k) {
+        const float4 v = *reinterpret_cast<const float4*>(p.part + paged_part_at<ROWS, D>(slot, r, c0 + 4 * k));
+        a[k].x += e * v.x;
+        a[k].y += e * v.y;
+        a[k].z += e * v.z;
+        a[k].w += e * v.w;
+      }
     }
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t row = paged_out_row(p, w.r.t0, w.tile * ROWS + r, w.h);
-    *reinterpret_cast<uint2*>(p.o + row * D + c4) =
-        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-    if (p.lse && c4 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+    const int64_t row = paged_out_row(p, cut.t0, cut.row0 + r, cut.h);
+#pragma unroll
+    for (int k = 0; k < COLS; ++k)
+      *reinterpret_cast<uint2*>(p.o + row * D + c0 + 4 * k) =
+          make_uint2(pack_bf16x2(a[k].x * inv, a[k].y * inv), pack_bf16x2(a[k].z * inv, a[k].w * inv));
+    if (p.lse && c0 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
   }
 }
 

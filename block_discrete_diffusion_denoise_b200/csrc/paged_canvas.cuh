@@ -4,13 +4,14 @@
 // A unit is 4 x 256 x 64 x D operations against 4 x 64 x D bytes of K and V, so
 // the tensor core bounds it.  Two 128-row tiles of queries stay in shared
 // memory and share every K and V block; S = Q K^T and O += P V go to TMEM
-// (2 x 64 + 2 x D columns), one softmax thread per row.  In the steady state
-// the tensor core runs
-//   S_0(j) PV_0(j-1) S_1(j) PV_1(j-1) S_0(j+1) ...
-// so that a tile's softmax has the other tile's products and its own next
-// scores to hide behind.  The warps are a persistent pipeline over the CTA's
-// stretch of units (paged_attention.cuh); each role walks it by itself, and a
-// word per unit tells the softmax warps which keys the producers found.
+// (2 x 64 + 2 x D columns), one softmax thread per row.  Each query tile has an
+// MMA warp of its own, which issues S(j) and then PV(j-1), so that a tile's
+// softmax hides behind its next scores and the other tile's products.  (One
+// warp for both tiles spent its time on the waits: 78 cycles for a barrier
+// that is ready, 30 for a commit, 2800 for a unit.)  The warps are a
+// persistent pipeline over the CTA's stretch of units (paged_attention.cuh);
+// each role walks it by itself, and a word per unit tells the softmax warps
+// which keys the producers found.
 #pragma once
 
 #include "paged_attention.cuh"
@@ -20,7 +21,8 @@ namespace dg {
 constexpr int CV_TILE = 128;             // packed rows of a query tile (MMA M)
 constexpr int CV_ROWS = 2 * CV_TILE;
 constexpr int CV_MASKS = 8;               // ring of key masks, deeper than any role runs ahead
-constexpr int CV_SOFTMAX_WARP = 3;       // warps 0 K and Q, 1 V, 2 MMA, 3..6 and 7..10 softmax of tiles 0 and 1
+constexpr int CV_MMA_WARP = 2;           // warps 0 K, 1 V, 2 and 3 Q and MMA of tiles 0 and 1,
+constexpr int CV_SOFTMAX_WARP = 4;       // 4..7 and 8..11 softmax of tiles 0 and 1
 constexpr int CV_THREADS = 32 * (CV_SOFTMAX_WARP + 8);
 constexpr float CV_RESCALE_LOG2 = 8.f;
 
@@ -139,8 +141,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* tail = smem + C::TAIL_OFF;
-  uint64_t* q_full = reinterpret_cast<uint64_t*>(tail);
-  uint64_t* q_empty = q_full + 1;
+  uint64_t* q_full = reinterpret_cast<uint64_t*>(tail);  // [2]
   uint64_t* k_full = q_full + 2;
   uint64_t* k_empty = k_full + C::STAGES;
   uint64_t* v_full = k_empty + C::STAGES;
@@ -151,11 +152,11 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   uint64_t* p_full = s_free + 2;               // [2] softmax q -> MMA: P_q written
   uint64_t* o_done = p_full + 2;               // [2] MMA -> softmax q: O_q += P_q V complete
   uint64_t* o_free = o_done + 2;               // [2] softmax q -> MMA: O_q read at a tile's end
-  uint64_t* drain = o_free + 2;
+  uint64_t* drain = o_free + 2;                // [2]
   uint64_t* key_mask = reinterpret_cast<uint64_t*>(tail + 512);  // [CV_MASKS] keys of the unit that exist
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail + 960);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 964);
-  static_assert((2 + 4 * C::STAGES + CV_MASKS + 11) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
+  static_assert((2 + 4 * C::STAGES + CV_MASKS + 12) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
   static_assert(CV_MASKS >= C::STAGES + 4, "a mask is read before its slot comes round");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -163,27 +164,26 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     tma_prefetch_desc(&p.k_map);
     tma_prefetch_desc(&p.v_map);
     tma_prefetch_desc(&cp.q_map);
-    mbar_init(q_full, 1);
-    mbar_init(q_empty, 1);
     for (int s = 0; s < C::STAGES; ++s) {
       mbar_init(&k_full[s], 1);
-      mbar_init(&k_empty[s], 1);
+      mbar_init(&k_empty[s], 2);               // both MMA warps
       mbar_init(&v_full[s], 1);
-      mbar_init(&v_empty[s], 1);
+      mbar_init(&v_empty[s], 2);
     }
     for (int s = 0; s < CV_MASKS; ++s) mbar_init(&m_full[s], 1);
     for (int q = 0; q < 2; ++q) {
+      mbar_init(&q_full[q], 1);
+      mbar_init(&drain[q], 1);
       mbar_init(&s_full[q], 1);
       mbar_init(&s_free[q], CV_TILE);
       mbar_init(&p_full[q], CV_TILE);
       mbar_init(&o_done[q], 1);
       mbar_init(&o_free[q], CV_TILE);
     }
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 2) {
+  if (warp == CV_MMA_WARP) {
     tmem_alloc(tmem_holder, C::TMEM_COLS);
     tmem_relinquish();
   }
@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   bool ok = true;
 
   if (warp < 2) {
-    // -------------------- producers: warp 0 Q and K, warp 1 V --------------------
+    // ----------------------- producers: warp 0 K, warp 1 V -----------------------
     const bool is_k = warp == 0;
     const CUtensorMap* map = is_k ? &p.k_map : &p.v_map;
     uint64_t* full = is_k ? k_full : v_full;
@@ -209,21 +209,10 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     const uint64_t pol = policy_evict_last();                   // the request's other row tiles read the block again
     int it = 0, seg = 0;
     uint32_t issued = 0, par = 0;
+    PagedCut cut{};
     for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+      cut = paged_cut<CV_ROWS>(p, g, w, seg);
       const int32_t* tab = p.table + w.b * p.table_stride;
-      const int row0 = w.tile * CV_ROWS;
-      const int nq = w.r.n * G - row0 > CV_TILE ? 2 : 1;
-      if (is_k) {
-        ok = __all_sync(0xffffffffu, (seg == 0 || mbar_wait(q_empty, (seg - 1) & 1, p.err)) && !*abort_flag);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(q_full, nq * C::Q_BYTES);
-        __syncwarp();
-        if (lane < nq * C::DK) {
-          const int q = lane / C::DK, b = lane % C::DK;
-          tma_load_4d(smem + q * C::Q_BYTES + b * CV_TILE * 128, &cp.q_map, q_full, b * 64, 0, w.h,
-                      w.r.t0 + (row0 + q * CV_TILE) / G, pol);
-        }
-      }
       int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         const int s = it % C::STAGES;
@@ -265,86 +254,111 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     if (lane == 0) {
       for (int s = 0; s < C::STAGES; ++s)
         if (issued >> s & 1) mbar_wait(&full[s], par >> s & 1, p.err);
-      if (is_k && seg > 0 && !ok) mbar_wait(q_full, (seg - 1) & 1, p.err);
+      if (!is_k) p.cuts[blockIdx.x] = cut;
     }
-  } else if (warp == 2) {
-    // -------------------------------- MMA issuer --------------------------------
+  } else if (warp < CV_SOFTMAX_WARP) {
+    // ------------------- MMA issuer of tile q, and its queries -------------------
     constexpr uint32_t IDESC_S = umma_idesc_bf16(CV_TILE, PG_BK);             // Q, K both K-major
     constexpr uint32_t IDESC_PV = umma_idesc_bf16(CV_TILE, D) | (1u << 16);   // V is MN-major
     const uint32_t lead = elect_one();
     const uint32_t at = smem_u32(smem), tmem = __shfl_sync(0xffffffffu, tmem_base, 0);
-    const UmmaOperand q_op(umma_desc_sw128(at)), k_op(umma_desc_sw128(at + C::K_OFF));
-    const UmmaOperand p_op(umma_desc_sw128(at + C::P_OFF)), v_op(umma_desc_sw128_mn(at + C::V_OFF, PG_BK * 128));
-    int n0 = 0, n1 = 0;                      // scores of tile 0 and of tile 1 so far (P V is one behind)
-    int held0 = 0, held1 = 0;                // row tiles that have used O_0, O_1
-    // S_q = Q_q K^T of unit j; n: the tile's number of them so far
-    auto scores = [&](int q, int j, int n) {
-      if (n > 0 && !mbar_wait_warp(&s_free[q], (n - 1) & 1, p.err)) return false;
-      tc_fence_after();
-      UmmaOperand a = q_op, b = k_op;
-      a.lo += (q * C::Q_BYTES) >> 4;
-      b.lo += ((j % C::STAGES) * C::KV_BYTES) >> 4;
-      const uint32_t d = tmem + C::S_COL + q * PG_BK;
-      umma_at<false>(lead, d, a, 0, b, 0, IDESC_S);
-#pragma unroll
-      for (int kk = 1; kk < D / 16; ++kk)
-        umma_at<true>(lead, d, a, (kk >> 2) * (CV_TILE * 128) + (kk & 3) * 32, b,
-                      (kk >> 2) * (PG_BK * 128) + (kk & 3) * 32, IDESC_S);
-      umma_commit_lead(lead, &s_full[q]);
-      return true;
+    const int q = __shfl_sync(0xffffffffu, warp - CV_MMA_WARP, 0);
+    UmmaOperand q_op(umma_desc_sw128(at)), p_op(umma_desc_sw128(at + C::P_OFF));
+    q_op.lo += (q * C::Q_BYTES) >> 4;
+    p_op.lo += (q * C::P_BYTES) >> 4;
+    const UmmaOperand k_op(umma_desc_sw128(at + C::K_OFF)), v_op(umma_desc_sw128_mn(at + C::V_OFF, PG_BK * 128));
+    int n = 0;                               // score tiles so far (P V is one behind)
+    int held = 0;                            // row tiles so far that have used O
+    int loads = 0;                           // row tiles so far whose queries were fetched
+    // the queries of a row tile, into shared memory that no product reads any more
+    auto fetch_q = [&](const PagedWalk<CV_ROWS>& w) {
+      if (lead) mbar_arrive_expect_tx(&q_full[q], C::Q_BYTES);
+      __syncwarp();
+      if (lane < C::DK)
+        tma_load_4d(smem + q * C::Q_BYTES + lane * CV_TILE * 128, &cp.q_map, &q_full[q], lane * 64, 0, w.h,
+                    w.r.t0 + (w.tile * CV_ROWS + q * CV_TILE) / G, policy_evict_last());
+      ++loads;
     };
-    // O_q (+)= P_q V of unit j, the tile's n-th; first: the row tile's first unit, behind `held` others
-    auto outputs = [&](int q, int j, int n, bool first, int held) {
-      if (!mbar_wait_warp(&p_full[q], n & 1, p.err)) return false;
-      if (first && held > 0 && !mbar_wait_warp(&o_free[q], (held - 1) & 1, p.err)) return false;
-      tc_fence_after();
-      UmmaOperand a = p_op, b = v_op;
-      a.lo += (q * C::P_BYTES) >> 4;
-      b.lo += ((j % C::STAGES) * C::KV_BYTES) >> 4;
-      const uint32_t d = tmem + C::O_COL + q * D;
-      if (first)
-        umma_at<false>(lead, d, a, 0, b, 0, IDESC_PV);
-      else
-        umma_at<true>(lead, d, a, 0, b, 0, IDESC_PV);
-#pragma unroll
-      for (int kk = 1; kk < PG_BK / 16; ++kk) umma_at<true>(lead, d, a, kk * 32, b, kk * 2048, IDESC_PV);
-      umma_commit_lead(lead, &o_done[q]);
-      return true;
-    };
-    int j = 0, seg = 0;
-    for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
-      const int two = __shfl_sync(0xffffffffu, w.r.n * G - w.tile * CV_ROWS > CV_TILE, 0);
+    auto has_rows = [&](const PagedWalk<CV_ROWS>& w) { return w.r.n * G - w.tile * CV_ROWS > q * CV_TILE; };
+    bool fetched = false;                    // this tile's queries are on their way
+    int j = 0;
+    for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p)) {
       const int units = __shfl_sync(0xffffffffu, w.kb1 - w.kb0, 0);
-      ok = mbar_wait_warp(q_full, seg & 1, p.err);
-      // unit u's scores, then the products of unit u - 1
-      for (int u = 0; ok && u <= units; ++u, ++j) {
-        const int ks = j % C::STAGES, vs = (j + C::STAGES - 1) % C::STAGES;
-        const bool has_s = u < units, has_o = u > 0;
-        if (has_s)
-          ok = __all_sync(0xffffffffu, !*abort_flag) && mbar_wait_warp(&k_full[ks], (j / C::STAGES) & 1, p.err) &&
-               scores(0, j, n0++);
-        if (ok && has_s && !two) umma_commit_lead(lead, &k_empty[ks]);
-        if (ok && has_o)
-          ok = mbar_wait_warp(&v_full[vs], ((j - 1) / C::STAGES) & 1, p.err) &&
-               outputs(0, j - 1, n0 - 1 - has_s, u == 1, held0);
-        if (two) {
-          if (ok && has_s) {
-            ok = scores(1, j, n1++);
-            if (ok) umma_commit_lead(lead, &k_empty[ks]);
-          }
-          if (ok && has_o) ok = outputs(1, j - 1, n1 - 1 - has_s, u == 1, held1);
+      if (!__shfl_sync(0xffffffffu, has_rows(w), 0)) {
+        // the other tile's blocks: pass them on
+        for (int u = 0; ok && u < units; ++u, ++j) {
+          const int st = j % C::STAGES, ph = (j / C::STAGES) & 1;
+          ok = mbar_wait_warp(&k_full[st], ph, p.err);
+          if (lead && ok) mbar_arrive(&k_empty[st]);
+          ok = ok && mbar_wait_warp(&v_full[st], ph, p.err);
+          if (lead && ok) mbar_arrive(&v_empty[st]);
         }
-        if (ok && has_o) umma_commit_lead(lead, &v_empty[vs]);
-        if (ok && u == units - 1) umma_commit_lead(lead, q_empty);
+        continue;
+      }
+      if (!fetched) fetch_q(w);
+      fetched = false;
+      ok = mbar_wait_warp(&q_full[q], (loads - 1) & 1, p.err);
+      // unit u's scores, then the product of unit u - 1
+      for (int u = 0; ok && u <= units; ++u, ++j) {
+        if (u < units) {
+          const int ks = j % C::STAGES;
+          ok = mbar_wait_warp(&k_full[ks], (j / C::STAGES) & 1, p.err) &&
+               (n == 0 || mbar_wait_warp(&s_free[q], (n - 1) & 1, p.err));
+          if (!ok) break;
+          tc_fence_after();
+          UmmaOperand b = k_op;
+          b.lo += (ks * C::KV_BYTES) >> 4;
+          const uint32_t d = tmem + C::S_COL + q * PG_BK;
+          umma_at<false>(lead, d, q_op, 0, b, 0, IDESC_S);
+#pragma unroll
+          for (int kk = 1; kk < D / 16; ++kk)
+            umma_at<true>(lead, d, q_op, (kk >> 2) * (CV_TILE * 128) + (kk & 3) * 32, b,
+                          (kk >> 2) * (PG_BK * 128) + (kk & 3) * 32, IDESC_S);
+          umma_commit_lead(lead, &s_full[q]);
+          umma_commit_lead(lead, &k_empty[ks]);
+          ++n;
+        }
+        if (u == units - 1) {
+          // the next row tile's queries, once the scores just issued are read
+          PagedWalk<CV_ROWS> next = w;
+          next.next(p);
+          fetched = __shfl_sync(0xffffffffu, next.more() && has_rows(next), 0);
+          if (fetched) {
+            ok = mbar_wait_warp(&s_free[q], (n - 1) & 1, p.err);
+            if (!ok) break;
+            fetch_q(next);
+          }
+        }
+        if (u > 0) {
+          const int vs = (j - 1) % C::STAGES;
+          const bool first = u == 1;
+          const int i = n - 1 - (u < units);   // P of unit u - 1
+          ok = mbar_wait_warp(&v_full[vs], ((j - 1) / C::STAGES) & 1, p.err) &&
+               mbar_wait_warp(&p_full[q], i & 1, p.err) &&
+               (!first || held == 0 || mbar_wait_warp(&o_free[q], (held - 1) & 1, p.err));
+          if (!ok) break;
+          tc_fence_after();
+          UmmaOperand b = v_op;
+          b.lo += (vs * C::KV_BYTES) >> 4;
+          const uint32_t d = tmem + C::O_COL + q * D;
+          if (first)
+            umma_at<false>(lead, d, p_op, 0, b, 0, IDESC_PV);
+          else
+            umma_at<true>(lead, d, p_op, 0, b, 0, IDESC_PV);
+#pragma unroll
+          for (int kk = 1; kk < PG_BK / 16; ++kk) umma_at<true>(lead, d, p_op, kk * 32, b, kk * 2048, IDESC_PV);
+          umma_commit_lead(lead, &o_done[q]);
+          umma_commit_lead(lead, &v_empty[vs]);
+        }
       }
       --j;
-      ++held0;
-      held1 += two;
+      ++held;
     }
     if (!ok) *abort_flag = 1;
-    // every MMA issued has completed before TMEM or its operands are released
-    umma_commit_lead(lead, drain);
-    mbar_wait_warp(drain, 0, p.err);
+    // every copy and MMA issued here has completed before shared memory and TMEM are released
+    if (loads > 0) mbar_wait_warp(&q_full[q], (loads - 1) & 1, p.err);
+    umma_commit_lead(lead, &drain[q]);
+    mbar_wait_warp(&drain[q], 0, p.err);
   } else {
     // ----------------------- softmax warpgroup of tile wg -----------------------
     const int wg = (warp - CV_SOFTMAX_WARP) >> 2;
@@ -491,7 +505,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   tc_fence_before();
   __syncthreads();
   if (*abort_flag) paged_poison<CV_ROWS, D>(p, g);
-  if (warp == 2) {
+  if (warp == CV_MMA_WARP) {
     __syncwarp();
     tc_fence_after();
     tmem_dealloc(tmem_base, C::TMEM_COLS);
