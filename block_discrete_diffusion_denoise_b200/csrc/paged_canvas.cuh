@@ -153,10 +153,11 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   uint64_t* o_done = p_full + 2;               // [2] MMA -> softmax q: O_q += P_q V complete
   uint64_t* o_free = o_done + 2;               // [2] softmax q -> MMA: O_q read at a tile's end
   uint64_t* drain = o_free + 2;                // [2]
+  uint64_t* turn = drain + 2;                  // [2][4] warp w of the other warpgroup has left its exponentials
   uint64_t* key_mask = reinterpret_cast<uint64_t*>(tail + 512);  // [CV_MASKS] keys of the unit that exist
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail + 960);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 964);
-  static_assert((2 + 4 * C::STAGES + CV_MASKS + 12) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
+  static_assert((2 + 4 * C::STAGES + CV_MASKS + 20) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
   static_assert(CV_MASKS >= C::STAGES + 4, "a mask is read before its slot comes round");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -179,6 +180,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       mbar_init(&p_full[q], CV_TILE);
       mbar_init(&o_done[q], 1);
       mbar_init(&o_free[q], CV_TILE);
+      for (int x = 0; x < 4; ++x) mbar_init(&turn[q * 4 + x], 1);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -368,12 +370,14 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     const uint32_t s_col = t_row + C::S_COL + wg * PG_BK, o_col = t_row + C::O_COL + wg * D;
     uint8_t* pdst = smem + C::P_OFF + wg * C::P_BYTES + rloc * 128;
     int j = 0, seg = 0, n_s = 0;                     // units of the stretch, tiles, score tiles read so far
+    int turns = 0;                                   // units so far that both tiles had rows in
     for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
       const int row0 = w.tile * CV_ROWS, units = w.kb1 - w.kb0;
       if (w.r.n * G - row0 <= wg * CV_TILE) {        // no live row in this tile
         j += units;
         continue;
       }
+      const bool both = w.r.n * G - row0 > CV_TILE;
       const int r = row0 + wg * CV_TILE + rloc;      // packed row of the request
       const bool live = r < w.r.n * G;
       // keys [0, lim) are this row's
@@ -383,10 +387,10 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       for (int u = 0; u < units; ++u, ++j, ++n_s) {
         const int key0 = (w.kb0 + u) * PG_BK;
         // warp-uniform decisions: tcgen05.ld below is a warp-collective
-        ok = __all_sync(0xffffffffu, mbar_wait(&m_full[j % CV_MASKS], (j / CV_MASKS) & 1, p.err));
-        const uint64_t valid = key_mask[j % CV_MASKS];
-        ok = ok && __all_sync(0xffffffffu, mbar_wait(&s_full[wg], n_s & 1, p.err) && !*abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait(&m_full[j % CV_MASKS], (j / CV_MASKS) & 1, p.err) &&
+                                         mbar_wait(&s_full[wg], n_s & 1, p.err));
         if (!ok) break;
+        const uint64_t valid = key_mask[j % CV_MASKS];
         tc_fence_after();
         float s[PG_BK];
         tmem_ld64(s_col, s);
@@ -409,6 +413,9 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
         if (resc) mref = mblk;
         const float base = mref == -INFINITY ? 0.f : mref;
         const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2), base2 = f32x2(-base, -base);
+        // The two warps of an SM quarter take turns at the exponentials, tile 0 first: without that they fall into
+        // step, share the MUFU at half speed and leave it and the tensor core idle together (2550 cycles a unit).
+        if (both) ok = mbar_wait(&turn[wg * 4 + quarter], (turns & 1) ^ (wg == 0), p.err);
         uint64_t l2[2] = {0, 0};
         uint32_t pk[PG_BK / 2];
 #pragma unroll
@@ -420,12 +427,17 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
           l2[c & 1] = f32x2_add(l2[c & 1], f32x2(p0, p1));
           pk[c] = cvt_bf16x2(p0, p1);
         }
+        if (both) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&turn[(wg ^ 1) * 4 + quarter]);
+          ++turns;
+        }
         float l0, l1;
         f32x2_split(f32x2_add(l2[0], l2[1]), l0, l1);
         lsum = lsum * factor + (l0 + l1);
         if (u > 0) {
           // O_q += P_q V of the unit before has completed: O_q is stable and P_q's buffer free
-          ok = __all_sync(0xffffffffu, mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err));
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err));
           if (!ok) break;
           tc_fence_after();
           if (__any_sync(0xffffffffu, resc)) {
@@ -464,7 +476,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       if (!ok) break;
 
       // ------------- the tile's end: its rows, or their partial slot -------------
-      ok = __all_sync(0xffffffffu, mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err) && !*abort_flag);
+      ok = __all_sync(0xffffffffu, ok && mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err));
       if (!ok) break;
       tc_fence_after();
       const bool whole = w.whole();
