@@ -146,8 +146,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   uint64_t* k_empty = k_full + C::STAGES;
   uint64_t* v_full = k_empty + C::STAGES;
   uint64_t* v_empty = v_full + C::STAGES;
-  uint64_t* m_full = v_empty + C::STAGES;      // [CV_MASKS] K producer -> softmax: key mask written
-  uint64_t* s_full = m_full + CV_MASKS;        // [2] MMA -> softmax q: scores ready
+  uint64_t* s_full = v_empty + C::STAGES;      // [2] MMA -> softmax q: scores ready, key mask written
   uint64_t* s_free = s_full + 2;               // [2] softmax q -> MMA: scores in registers
   uint64_t* p_full = s_free + 2;               // [2] softmax q -> MMA: P_q written
   uint64_t* o_done = p_full + 2;               // [2] MMA -> softmax q: O_q += P_q V complete
@@ -157,7 +156,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   uint64_t* key_mask = reinterpret_cast<uint64_t*>(tail + 512);  // [CV_MASKS] keys of the unit that exist
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tail + 960);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 964);
-  static_assert((2 + 4 * C::STAGES + CV_MASKS + 20) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
+  static_assert((2 + 4 * C::STAGES + 20) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
   static_assert(CV_MASKS >= C::STAGES + 4, "a mask is read before its slot comes round");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -171,15 +170,14 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       mbar_init(&v_full[s], 1);
       mbar_init(&v_empty[s], 2);
     }
-    for (int s = 0; s < CV_MASKS; ++s) mbar_init(&m_full[s], 1);
     for (int q = 0; q < 2; ++q) {
       mbar_init(&q_full[q], 1);
       mbar_init(&drain[q], 1);
-      mbar_init(&s_full[q], 1);
-      mbar_init(&s_free[q], CV_TILE);
-      mbar_init(&p_full[q], CV_TILE);
+      mbar_init(&s_full[q], 2);                // the products' commit, and the warp that has seen the mask
+      mbar_init(&s_free[q], 4);                // a lane of each softmax warp
+      mbar_init(&p_full[q], 4);
       mbar_init(&o_done[q], 1);
-      mbar_init(&o_free[q], CV_TILE);
+      mbar_init(&o_free[q], 4);
       for (int x = 0; x < 4; ++x) mbar_init(&turn[q * 4 + x], 1);
     }
     *abort_flag = 0;
@@ -230,7 +228,6 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err) && !*abort_flag);
         if (!ok) break;
         if (lane == 0) {
-          mbar_arrive_expect_tx(&full[s], __popc(pmask) * box * 128 * C::DK);
           if (is_k) {
             uint64_t valid = 0;
             for (int i = 0; i < pieces; ++i)
@@ -240,8 +237,8 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
             // the slot's last reader has read it: this K slot came free STAGES units behind it, and the softmax of a
             // tile is never more than two units behind its scores
             key_mask[it % CV_MASKS] = valid;
-            mbar_arrive(&m_full[it % CV_MASKS]);
           }
+          mbar_arrive_expect_tx(&full[s], __popc(pmask) * box * 128 * C::DK);
         }
         __syncwarp();
         if (db < C::DK && good)
@@ -318,6 +315,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
                           (kk >> 2) * (PG_BK * 128) + (kk & 3) * 32, IDESC_S);
           umma_commit_lead(lead, &s_full[q]);
           umma_commit_lead(lead, &k_empty[ks]);
+          if (lead) mbar_arrive(&s_full[q]);
           ++n;
         }
         if (u == units - 1) {
@@ -387,15 +385,15 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       for (int u = 0; u < units; ++u, ++j, ++n_s) {
         const int key0 = (w.kb0 + u) * PG_BK;
         // warp-uniform decisions: tcgen05.ld below is a warp-collective
-        ok = __all_sync(0xffffffffu, mbar_wait(&m_full[j % CV_MASKS], (j / CV_MASKS) & 1, p.err) &&
-                                         mbar_wait(&s_full[wg], n_s & 1, p.err));
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[wg], n_s & 1, p.err));
         if (!ok) break;
         const uint64_t valid = key_mask[j % CV_MASKS];
         tc_fence_after();
         float s[PG_BK];
         tmem_ld64(s_col, s);
         tc_fence_before();
-        mbar_arrive(&s_free[wg]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_free[wg]);
         if (key0 + PG_BK > lim_all || valid != ~uint64_t(0)) {
           const int lj = lim - key0;
 #pragma unroll
@@ -471,7 +469,8 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
               make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
         fence_proxy_async_smem();
         tc_fence_before();
-        mbar_arrive(&p_full[wg]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[wg]);
       }
       if (!ok) break;
 
@@ -504,7 +503,8 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
         }
       }
       tc_fence_before();
-      mbar_arrive(&o_free[wg]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&o_free[wg]);
       if (live) {
         if (!whole)
           p.part_ml[slot * CV_ROWS + wg * CV_TILE + rloc] = make_float2(mref, lsum);
