@@ -410,32 +410,9 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
         const float factor = resc ? ex2_approx(mref - mblk) : 1.f;  // 0 when mref = -inf
         if (resc) mref = mblk;
         const float base = mref == -INFINITY ? 0.f : mref;
-        const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2), base2 = f32x2(-base, -base);
-        // The two warps of an SM quarter take turns at the exponentials, tile 0 first: without that they fall into
-        // step, share the MUFU at half speed and leave it and the tensor core idle together (2550 cycles a unit).
-        if (both) ok = mbar_wait(&turn[wg * 4 + quarter], (turns & 1) ^ (wg == 0), p.err);
-        uint64_t l2[2] = {0, 0};
-        uint32_t pk[PG_BK / 2];
-#pragma unroll
-        for (int c = 0; c < PG_BK / 2; ++c) {
-          // p enters the second product in bf16 (2^-9 of each, averaging out over keys); its sum stays fp32
-          float x0, x1;
-          f32x2_split(f32x2_fma(f32x2(s[2 * c], s[2 * c + 1]), scale2, base2), x0, x1);
-          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          l2[c & 1] = f32x2_add(l2[c & 1], f32x2(p0, p1));
-          pk[c] = cvt_bf16x2(p0, p1);
-        }
-        if (both) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&turn[(wg ^ 1) * 4 + quarter]);
-          ++turns;
-        }
-        float l0, l1;
-        f32x2_split(f32x2_add(l2[0], l2[1]), l0, l1);
-        lsum = lsum * factor + (l0 + l1);
         if (u > 0) {
           // O_q += P_q V of the unit before has completed: O_q is stable and P_q's buffer free
-          ok = __all_sync(0xffffffffu, ok && mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err));
+          ok = __all_sync(0xffffffffu, mbar_wait(&o_done[wg], (n_s - 1) & 1, p.err));
           if (!ok) break;
           tc_fence_after();
           if (__any_sync(0xffffffffu, resc)) {
@@ -462,15 +439,40 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
               for (int b = 0; b < C::DK; ++b) reinterpret_cast<uint4*>(vb + b * PG_BK * 128)[i] = make_uint4(0, 0, 0, 0);
             }
         }
-        // row rloc of a K-major 128-byte-swizzled tile: 16-byte chunk c lands at c ^ (row & 7)
+        const uint64_t scale2 = f32x2(p.scale_log2, p.scale_log2), base2 = f32x2(-base, -base);
+        // The two warps of an SM quarter take turns at the exponentials, tile 0 first: without that they fall into
+        // step, share the MUFU at half speed and leave it and the tensor core idle together (2550 cycles a unit).
+        if (both) ok = mbar_wait(&turn[wg * 4 + quarter], (turns & 1) ^ (wg == 0), p.err);
+        uint64_t l2[2] = {0, 0};
 #pragma unroll
-        for (int ch = 0; ch < 8; ++ch)
-          *reinterpret_cast<uint4*>(pdst + ((ch ^ (rloc & 7)) << 4)) =
-              make_uint4(pk[4 * ch], pk[4 * ch + 1], pk[4 * ch + 2], pk[4 * ch + 3]);
+        for (int ch = 0; ch < 8; ++ch) {
+          uint32_t pk[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // p enters the second product in bf16 (2^-9 of each, averaging out over keys); its sum stays fp32
+            float x0, x1;
+            f32x2_split(f32x2_fma(f32x2(s[8 * ch + 2 * c], s[8 * ch + 2 * c + 1]), scale2, base2), x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            l2[c & 1] = f32x2_add(l2[c & 1], f32x2(p0, p1));
+            pk[c] = cvt_bf16x2(p0, p1);
+          }
+          // row rloc of a K-major 128-byte-swizzled tile: 16-byte chunk c lands at c ^ (row & 7)
+          *reinterpret_cast<uint4*>(pdst + ((ch ^ (rloc & 7)) << 4)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+        }
+        if (both) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&turn[(wg ^ 1) * 4 + quarter]);
+          ++turns;
+        }
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[wg]);
+        float l0, l1;
+        f32x2_split(f32x2_add(l2[0], l2[1]), l0, l1);
+        lsum = lsum * factor + (l0 + l1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
       }
       if (!ok) break;
 
@@ -482,25 +484,33 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
       const int64_t row = live ? paged_out_row(p, w.r.t0, r, w.h) : 0;
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0);
-#pragma unroll 1
-      for (int c0 = 0; c0 < D; c0 += 16) {
-        float v[16];
-        tmem_ld16(o_col + c0, v);
-        if (!live) continue;
+      // columns [c0, c0 + N) of the row
+      auto put = [&](int c0, auto& v) {
+        constexpr int N = sizeof(v) / sizeof(float);
+        if (!live) return;
         if (whole) {
           uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c0);
 #pragma unroll
-          for (int e = 0; e < 16; ++e) v[e] *= inv;
-          dst[0] = make_uint4(cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3]), cvt_bf16x2(v[4], v[5]),
-                              cvt_bf16x2(v[6], v[7]));
-          dst[1] = make_uint4(cvt_bf16x2(v[8], v[9]), cvt_bf16x2(v[10], v[11]), cvt_bf16x2(v[12], v[13]),
-                              cvt_bf16x2(v[14], v[15]));
+          for (int e = 0; e < N; e += 8)
+            dst[e / 8] = make_uint4(cvt_bf16x2(v[e] * inv, v[e + 1] * inv), cvt_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
+                                    cvt_bf16x2(v[e + 4] * inv, v[e + 5] * inv), cvt_bf16x2(v[e + 6] * inv, v[e + 7] * inv));
         } else {
+          float4* dst = reinterpret_cast<float4*>(p.part + paged_part_at<CV_ROWS, D>(slot, wg * CV_TILE + rloc, c0));
 #pragma unroll
-          for (int e = 0; e < 16; e += 4)
-            *reinterpret_cast<float4*>(p.part + paged_part_at<CV_ROWS, D>(slot, wg * CV_TILE + rloc, c0 + e)) =
-                make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          for (int e = 0; e < N; e += 4) dst[e / 4 * CV_ROWS] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
+      };
+#pragma unroll 1
+      for (int c0 = 0; c0 + 64 <= D; c0 += 64) {
+        float v[64];
+        tmem_ld64(o_col + c0, v);
+        put(c0, v);
+      }
+#pragma unroll
+      for (int c0 = D / 64 * 64; c0 < D; c0 += 16) {
+        float v[16];
+        tmem_ld16(o_col + c0, v);
+        put(c0, v);
       }
       tc_fence_before();
       __syncwarp();
