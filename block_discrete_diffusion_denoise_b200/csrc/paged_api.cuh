@@ -138,18 +138,24 @@ bool make_map_rows(CUtensorMap* m, const dg_paged_attention_args* a) {
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D>
-dg_status launch_token(const PagedAttnParams& p, int sms, void* stream) {
-  const dg_status st = paged_launch(paged_token_kernel<D>, dim3(sms), TOK_THREADS, TokCfg<D>::SMEM, stream, p);
-  if (st != DG_OK) return st;
-  return paged_launch(paged_merge_kernel<TOK_ROWS, D>, dim3(sms), PG_MERGE_THREADS, 0, stream, p, true);
+// the merge's CTAs: one per tile where the call has no more tiles than the device SMs, else one per SM
+template <int ROWS, int D>
+dg_status launch_merge(const PagedAttnParams& p, int tiles, int sms, void* stream) {
+  using C = MergeCfg<ROWS>;
+  const dim3 grid(p.cuts_by_tile ? tiles : sms, ROWS == TOK_ROWS ? 1 : D / 4 / C::COLS);
+  return paged_launch(paged_merge_kernel<ROWS, D>, grid, C::THREADS, 0, stream, p, true);
 }
 
 template <int D>
-dg_status launch_canvas(const CanvasParams& p, int sms, void* stream) {
+dg_status launch_token(const PagedAttnParams& p, int tiles, int sms, void* stream) {
+  const dg_status st = paged_launch(paged_token_kernel<D>, dim3(sms), TOK_THREADS, TokCfg<D>::SMEM, stream, p);
+  return st != DG_OK ? st : launch_merge<TOK_ROWS, D>(p, tiles, sms, stream);
+}
+
+template <int D>
+dg_status launch_canvas(const CanvasParams& p, int tiles, int sms, void* stream) {
   const dg_status st = paged_launch(paged_canvas_kernel<D>, dim3(sms), CV_THREADS, CvCfg<D>::SMEM, stream, p);
-  if (st != DG_OK) return st;
-  return paged_launch(paged_merge_kernel<CV_ROWS, D>, dim3(sms, D / 16), PG_MERGE_THREADS, 0, stream, p.a, true);
+  return st != DG_OK ? st : launch_merge<CV_ROWS, D>(p.a, tiles, sms, stream);
 }
 
 }  // namespace
@@ -281,10 +287,16 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   p.causal = a->causal != 0;
   p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
   p.err = DevErr{nullptr, 1000000000ull};
+  // tiles: ceil(rows_b * G / ROWS) over the requests, per kv head
+  const int64_t tile_rows = few ? TOK_ROWS : CV_ROWS;
+  const int64_t tiles64 =
+      (static_cast<int64_t>(a->n_rows) * (a->n_q_heads / a->n_kv_heads) / tile_rows + a->batch) * a->n_kv_heads;
+  const int tiles = static_cast<int>(std::min<int64_t>(tiles64, sms));
+  p.cuts_by_tile = tiles64 <= sms ? tiles : 0;
   switch (a->head_dim) {
-    case 64: return few ? launch_token<64>(p, sms, cuda_stream) : launch_canvas<64>(cp, sms, cuda_stream);
-    case 128: return few ? launch_token<128>(p, sms, cuda_stream) : launch_canvas<128>(cp, sms, cuda_stream);
-    default: return few ? launch_token<176>(p, sms, cuda_stream) : launch_canvas<176>(cp, sms, cuda_stream);
+    case 64: return few ? launch_token<64>(p, tiles, sms, cuda_stream) : launch_canvas<64>(cp, tiles, sms, cuda_stream);
+    case 128: return few ? launch_token<128>(p, tiles, sms, cuda_stream) : launch_canvas<128>(cp, tiles, sms, cuda_stream);
+    default: return few ? launch_token<176>(p, tiles, sms, cuda_stream) : launch_canvas<176>(cp, tiles, sms, cuda_stream);
   }
 }
 

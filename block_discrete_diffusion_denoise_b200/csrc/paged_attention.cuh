@@ -24,9 +24,9 @@ constexpr int PG_BK = 64;      // keys per unit
 struct PagedCut {
   int rows;                    // live packed rows of the tile
   int t0, row0, h;             // the request's first row, the tile's first packed row, kv head
-  int slot;                    // partial slot of the first piece
-  int last;                    // CTA of the last piece (the others are slot 2 c of the CTAs up to it)
-  int pad[2];
+  int first, slot;             // CTA and partial slot of the first piece
+  int last;                    // CTA of the last piece (the pieces between: slot 2 c of CTA c)
+  int tiles;                   // tiles of the whole call
 };
 
 struct PagedAttnParams {
@@ -42,8 +42,9 @@ struct PagedAttnParams {
   float* lse;                  // [rows][Hq] or null
   float* part;                 // [CTA][2][tile rows][D] raw rows of cut tiles
   float2* part_ml;             // [CTA][2][tile rows] their (max in log2 units, sum)
-  PagedCut* cuts;              // [CTA]
+  PagedCut* cuts;              // [CTA], or with cuts_by_tile [tile]
   int rows, batch, Hq, Hkv, n_pages, page_shift, width, causal;
+  int cuts_by_tile;            // entries of `cuts` by tile where the call has at most as many tiles as CTAs, else 0
   float scale_log2;            // log2(e) * scale
   DevErr err;
 };
@@ -87,6 +88,7 @@ __device__ __forceinline__ long long paged_units(const PagedAttnParams& p, const
 struct PagedRange {
   int64_t lo, hi, rem, total;
   int b, ctas;
+  int tiles, tiles0;           // of the call, of the requests before b
 };
 
 // One pass over the batch by the whole CTA: each thread sums the units of a
@@ -94,46 +96,71 @@ struct PagedRange {
 template <int ROWS>
 __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int cta, int ctas) {
   __shared__ long long warp_sum[32];
+  __shared__ int warp_tiles[32];
   __shared__ long long found_rem;
-  __shared__ int found_b;
+  __shared__ int found_b, found_tiles;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int per = (p.batch + blockDim.x - 1) / blockDim.x;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
   long long sum = 0;
-  for (int b = b0; b < b1; ++b) sum += paged_units<ROWS>(p, paged_request<ROWS>(p, b));
+  int tiles = 0;
+  for (int b = b0; b < b1; ++b) {
+    const PagedRequest r = paged_request<ROWS>(p, b);
+    sum += paged_units<ROWS>(p, r);
+    tiles += r.tiles * p.Hkv;
+  }
   long long upto = sum;
+  int tiles_upto = tiles;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-    if (lane >= o) upto += x;
+    const int y = __shfl_up_sync(0xffffffffu, tiles_upto, o);
+    if (lane >= o) {
+      upto += x;
+      tiles_upto += y;
+    }
   }
-  if (lane == 31) warp_sum[warp] = upto;
+  if (lane == 31) {
+    warp_sum[warp] = upto;
+    warp_tiles[warp] = tiles_upto;
+  }
   __syncthreads();
   long long total = 0, before = 0;
+  int tiles_all = 0, tiles_before = 0;
   for (int w = 0; w < warps; ++w) {
-    if (w < warp) before += warp_sum[w];
+    if (w < warp) {
+      before += warp_sum[w];
+      tiles_before += warp_tiles[w];
+    }
     total += warp_sum[w];
+    tiles_all += warp_tiles[w];
   }
   PagedRange g;
   g.total = total;
+  g.tiles = tiles_all;
   g.ctas = static_cast<int>(min64(ctas, total));
   g.lo = cta < g.ctas ? total * cta / g.ctas : total;
   g.hi = cta < g.ctas ? total * (cta + 1) / g.ctas : total;
   long long at = before + upto - sum;
+  int tiles_at = tiles_before + tiles_upto - tiles;
   if (g.lo < g.hi && g.lo >= at && g.lo < at + sum) {
     for (int b = b0; b < b1; ++b) {
-      const long long u = paged_units<ROWS>(p, paged_request<ROWS>(p, b));
+      const PagedRequest r = paged_request<ROWS>(p, b);
+      const long long u = paged_units<ROWS>(p, r);
       if (g.lo < at + u) {
         found_b = b;
         found_rem = g.lo - at;
+        found_tiles = tiles_at;
         break;
       }
       at += u;
+      tiles_at += r.tiles * p.Hkv;
     }
   }
   __syncthreads();
   g.b = g.lo < g.hi ? found_b : p.batch;
   g.rem = found_rem;
+  g.tiles0 = found_tiles;
   return g;
 }
 
@@ -144,6 +171,7 @@ struct PagedWalk {
   PagedRequest r;
   int64_t left;
   int b, tile, h, nb, kb0, kb1;
+  int ord;                     // number of the tile on the line
 
   __device__ __forceinline__ PagedWalk(const PagedAttnParams& p, const PagedRange& g) : left(g.hi - g.lo), b(g.b) {
     if (left <= 0) return;
@@ -162,6 +190,7 @@ struct PagedWalk {
       }
     }
     h = static_cast<int>(rem / nb);
+    ord = g.tiles0 + tile * p.Hkv + h;
     kb0 = static_cast<int>(rem % nb);
     kb1 = static_cast<int>(min64(nb, kb0 + left));
   }
@@ -171,6 +200,7 @@ struct PagedWalk {
     left -= kb1 - kb0;
     if (left <= 0) return;
     kb0 = 0;
+    ++ord;
     if (++h == p.Hkv) {
       h = 0;
       if (++tile == r.tiles) {
@@ -196,22 +226,29 @@ __device__ __forceinline__ int64_t paged_part_at(int64_t slot, int r, int c) {
   return ROWS == 16 ? (slot * ROWS + r) * D + c : ((slot * (D / 4) + c / 4) * ROWS + r) * 4 + c % 4;
 }
 
-// the tile that is left unfinished at the end of tile number seg of a stretch
+// Lists tile number seg of a stretch for the merge kernel, if it begins there:
+// with its pieces where the stretch does not finish it.  By tile, each has an
+// entry; by CTA, only the last one of a stretch can be unfinished, and the
+// caller writes `cut` in the end.
 template <int ROWS>
-__device__ __forceinline__ PagedCut paged_cut(const PagedAttnParams& p, const PagedRange& g, const PagedWalk<ROWS>& w,
-                                              int seg) {
-  PagedCut c{};
-  if (w.kb0 > 0 || w.kb1 == w.nb) return c;
-  c.rows = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
-  c.t0 = w.r.t0;
-  c.row0 = w.tile * ROWS;
-  c.h = w.h;
-  c.slot = 2 * blockIdx.x + (seg > 0);
-  // the pieces behind this one are the first of each stretch up to the one that holds the tile's last unit,
-  // end - 1: floor(W c / N) <= u is c <= ((u + 1) N - 1) / W
-  const int64_t end = g.hi + (w.nb - w.kb1);
-  c.last = static_cast<int>((end * g.ctas - 1) / g.total);
-  return c;
+__device__ __forceinline__ void paged_list(const PagedAttnParams& p, const PagedRange& g, const PagedWalk<ROWS>& w,
+                                           int seg, PagedCut& cut) {
+  cut = PagedCut{};
+  cut.tiles = g.tiles;
+  if (w.kb0 > 0) return;
+  if (w.kb1 < w.nb) {
+    cut.rows = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
+    cut.t0 = w.r.t0;
+    cut.row0 = w.tile * ROWS;
+    cut.h = w.h;
+    cut.first = blockIdx.x;
+    cut.slot = 2 * blockIdx.x + (seg > 0);
+    // the pieces behind this one are the first of each stretch up to the one that holds the tile's last unit,
+    // end - 1: floor(W c / N) <= u is c <= ((u + 1) N - 1) / W
+    const int64_t end = g.hi + (w.nb - w.kb1);
+    cut.last = static_cast<int>((end * g.ctas - 1) / g.total);
+  }
+  if (w.ord < p.cuts_by_tile) p.cuts[w.ord] = cut;   // more only where cu_rows decreases
 }
 
 // untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
@@ -301,8 +338,9 @@ template <int ROWS, int D>
 __device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
   int seg = 0;
   PagedCut cut{};
+  cut.tiles = g.tiles;
   for (PagedWalk<ROWS> w(p, g); w.more(); w.next(p), ++seg) {
-    cut = paged_cut<ROWS>(p, g, w, seg);
+    paged_list<ROWS>(p, g, w, seg, cut);   // every thread writes the same
     const int live = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
     for (int i = threadIdx.x; i < live * D; i += blockDim.x) {
       const int64_t out = paged_out_row(p, w.r.t0, w.tile * ROWS + i / D, w.h);
@@ -316,7 +354,7 @@ __device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
       }
     }
   }
-  if (threadIdx.x == 0) p.cuts[blockIdx.x] = cut;
+  if (threadIdx.x == 0 && !p.cuts_by_tile) p.cuts[blockIdx.x] = cut;
 }
 
 template <int D>
@@ -370,7 +408,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     uint32_t issued = 0, par = 0;
     PagedCut cut{};
     for (PagedWalk<TOK_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
-      cut = paged_cut<TOK_ROWS>(p, g, w, seg);
+      if (lane == 0) paged_list<TOK_ROWS>(p, g, w, seg, cut);
       const int32_t* tab = p.table + w.b * p.table_stride;
       const int live = min(w.r.n * G - w.tile * TOK_ROWS, TOK_ROWS);
       int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
@@ -427,7 +465,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       }
     }
     if (lane == 0) {
-      p.cuts[blockIdx.x] = cut;
+      if (!p.cuts_by_tile) p.cuts[blockIdx.x] = cut;
       const int s = it % C::STAGES;
       if (ok && mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err)) {
         desc[s].flags = TOK_EXIT;
@@ -606,53 +644,108 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
 // ----------------------------------------------------------------------------
 // Joins the tiles that the stretches cut, from the attention kernel's list:
 //   o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max_i m_i
-// over a tile's pieces in key order.  A thread takes COLS groups of four
-// columns of one row.  Launched while the attention kernel still runs.
+// over a tile's pieces, in one pass with a running maximum.  Bound by the
+// latency of its loads, of which each thread keeps several in flight; a small
+// tile's pieces are dealt out to groups of threads, joined in shared memory.
+// Launched while the attention kernel still runs.
 // ----------------------------------------------------------------------------
-constexpr int PG_MERGE_THREADS = 256;
 template <int ROWS>
-constexpr int paged_merge_cols() { return ROWS == 16 ? 1 : 4; }
+struct MergeCfg {
+  static constexpr int THREADS = ROWS == 16 ? 512 : 256;
+  static constexpr int COLS = ROWS == 16 ? 1 : 2;    // groups of four columns of a thread
+  static constexpr int DEEP = ROWS == 16 ? 8 : 5;    // pieces in flight
+};
+
+template <int COLS>
+struct MergeAcc {
+  float m = -INFINITY, l = 0.f;
+  float4 o[COLS];
+  __device__ __forceinline__ MergeAcc() {
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) o[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  __device__ __forceinline__ void add(float2 ml, const float4 (&v)[COLS]) {
+    const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+    const float e0 = ex2_approx(m - base), e1 = ex2_approx(ml.x - base);
+    m = mn;
+    l = l * e0 + ml.y * e1;
+#pragma unroll
+    for (int k = 0; k < COLS; ++k) {
+      o[k].x = o[k].x * e0 + v[k].x * e1;
+      o[k].y = o[k].y * e0 + v[k].y * e1;
+      o[k].z = o[k].z * e0 + v[k].z * e1;
+      o[k].w = o[k].w * e0 + v[k].w * e1;
+    }
+  }
+};
 
 template <int ROWS, int D>
-__global__ void __launch_bounds__(PG_MERGE_THREADS) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
+__global__ void __launch_bounds__(MergeCfg<ROWS>::THREADS) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
   DG_TIMELINE_SCOPE(TLK_ATTN_MERGE);
-  constexpr int COLS = paged_merge_cols<ROWS>(), GROUPS = D / 4 / COLS;
+  using C = MergeCfg<ROWS>;
+  __shared__ float4 s_o[ROWS == 16 ? C::THREADS : 1];
+  __shared__ float2 s_ml[ROWS == 16 ? C::THREADS : 1];
   pdl_wait();
+  // by tile, the first entry says how many there are
+  if (p.cuts_by_tile && static_cast<int>(blockIdx.x) >= p.cuts[0].tiles) return;
   const PagedCut cut = p.cuts[blockIdx.x];
-  for (int i = blockIdx.y * PG_MERGE_THREADS + threadIdx.x; i < ROWS * GROUPS; i += gridDim.y * PG_MERGE_THREADS) {
-    // neighbouring threads: columns of a row where the rows lie whole, else rows
-    const int r = ROWS == 16 ? i / GROUPS : i % ROWS, c0 = (ROWS == 16 ? i % GROUPS : i / ROWS) * COLS * 4;
-    if (r >= cut.rows) continue;
-    float M = p.part_ml[static_cast<int64_t>(cut.slot) * ROWS + r].x;
-#pragma unroll 4
-    for (int x = blockIdx.x + 1; x <= cut.last; ++x) M = fmaxf(M, p.part_ml[static_cast<int64_t>(2 * x) * ROWS + r].x);
-    const float base = M == -INFINITY ? 0.f : M;
-    float L = 0.f;
-    float4 a[COLS];
+  if (cut.rows == 0) return;
+  // items: a row's column group; neighbouring threads take columns of a row where rows lie whole, else rows
+  const int items = ROWS == 16 ? cut.rows * (D / 4) : ROWS;
+  const int groups = ROWS == 16 ? max(1, C::THREADS / items) : 1;
+  const int grp = ROWS == 16 && groups > 1 ? threadIdx.x / items : 0;
+  for (int i = threadIdx.x - grp * items; i < items; i += C::THREADS) {
+    const int r = ROWS == 16 ? i / (D / 4) : i;
+    const int c0 = ROWS == 16 ? i % (D / 4) * 4 : blockIdx.y * C::COLS * 4;
+    if (r >= cut.rows || grp >= groups) break;
+    MergeAcc<C::COLS> acc;
+    for (int x0 = cut.first + grp; x0 <= cut.last; x0 += groups * C::DEEP) {
+      float2 ml[C::DEEP];
+      float4 v[C::DEEP][C::COLS];
 #pragma unroll
-    for (int k = 0; k < COLS; ++k) a[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int x = blockIdx.x; x <= cut.last; ++x) {
-      const int64_t slot = x == blockIdx.x ? cut.slot : 2 * x;
-      const float2 ml = p.part_ml[slot * ROWS + r];
-      const float e = ex2_approx(ml.x - base);
-      L += e * ml.y;
+      for (int y = 0; y < C::DEEP; ++y) {
+        const int x = x0 + y * groups;
+        if (x > cut.last) break;
+        const int64_t slot = x == cut.first ? cut.slot : 2 * x;
+        ml[y] = p.part_ml[slot * ROWS + r];
 #pragma unroll
-      for (int k = 0; k < COLS; ++k) {
-        const float4 v = *reinterpret_cast<const float4*>(p.part + paged_part_at<ROWS, D>(slot, r, c0 + 4 * k));
-        a[k].x += e * v.x;
-        a[k].y += e * v.y;
-        a[k].z += e * v.z;
-        a[k].w += e * v.w;
+        for (int k = 0; k < C::COLS; ++k)
+          v[y][k] = *reinterpret_cast<const float4*>(p.part + paged_part_at<ROWS, D>(slot, r, c0 + 4 * k));
+      }
+#pragma unroll
+      for (int y = 0; y < C::DEEP; ++y) {
+        if (x0 + y * groups > cut.last) break;
+        acc.add(ml[y], v[y]);
       }
     }
-    const float inv = L == 0.f ? 0.f : 1.f / L;
+    if (ROWS == 16 && groups > 1) {
+      s_o[threadIdx.x] = acc.o[0];
+      s_ml[threadIdx.x] = make_float2(acc.m, acc.l);
+      break;   // one item per thread
+    }
+    const float inv = acc.l == 0.f ? 0.f : 1.f / acc.l;
     const int64_t row = paged_out_row(p, cut.t0, cut.row0 + r, cut.h);
 #pragma unroll
-    for (int k = 0; k < COLS; ++k)
+    for (int k = 0; k < C::COLS; ++k)
       *reinterpret_cast<uint2*>(p.o + row * D + c0 + 4 * k) =
-          make_uint2(pack_bf16x2(a[k].x * inv, a[k].y * inv), pack_bf16x2(a[k].z * inv, a[k].w * inv));
-    if (p.lse && c0 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
+          make_uint2(pack_bf16x2(acc.o[k].x * inv, acc.o[k].y * inv), pack_bf16x2(acc.o[k].z * inv, acc.o[k].w * inv));
+    if (p.lse && c0 == 0) p.lse[row] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * 0.69314718055994531f;
+  }
+  if (ROWS == 16 && groups > 1) {
+    __syncthreads();
+    const int i = threadIdx.x;
+    if (i >= items) return;
+    MergeAcc<1> acc;
+    for (int x = 0; x < groups; ++x) {
+      const float4 v[1] = {s_o[x * items + i]};
+      acc.add(s_ml[x * items + i], v);
+    }
+    const int r = i / (D / 4), c0 = i % (D / 4) * 4;
+    const float inv = acc.l == 0.f ? 0.f : 1.f / acc.l;
+    const int64_t row = paged_out_row(p, cut.t0, cut.row0 + r, cut.h);
+    *reinterpret_cast<uint2*>(p.o + row * D + c0) =
+        make_uint2(pack_bf16x2(acc.o[0].x * inv, acc.o[0].y * inv), pack_bf16x2(acc.o[0].z * inv, acc.o[0].w * inv));
+    if (p.lse && c0 == 0) p.lse[row] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * 0.69314718055994531f;
   }
 }
 

@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     uint32_t issued = 0, par = 0;
     PagedCut cut{};
     for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
-      cut = paged_cut<CV_ROWS>(p, g, w, seg);
+      if (!is_k && lane == 0) paged_list<CV_ROWS>(p, g, w, seg, cut);
       const int32_t* tab = p.table + w.b * p.table_stride;
       int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
@@ -253,7 +253,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     if (lane == 0) {
       for (int s = 0; s < C::STAGES; ++s)
         if (issued >> s & 1) mbar_wait(&full[s], par >> s & 1, p.err);
-      if (!is_k) p.cuts[blockIdx.x] = cut;
+      if (!is_k && !p.cuts_by_tile) p.cuts[blockIdx.x] = cut;
     }
   } else if (warp < CV_SOFTMAX_WARP) {
     // ------------------- MMA issuer of tile q, and its queries -------------------
