@@ -6,9 +6,8 @@
 //
 // Work is counted in units: one 64-key block of one tile (packed rows of one
 // request and kv head).  The units of a call form one line, in the order
-// (request, row tile, kv head, key block), and CTA c of N takes the stretch
-// [W c / N, W (c + 1) / N): every CTA has the same work whatever the lengths,
-// and the lengths are read on the device, so a captured launch serves any.  A
+// (request, row tile, kv head, key block), and the CTAs take stretches of equal
+// length of it: every CTA has the same work whatever the requests' lengths, and the lengths are read on the device, so a captured launch serves any.  A
 // tile that a stretch cuts leaves its raw rows and row statistics in a
 // partial slot (two per CTA: the stretch's first tile and its last), and
 // the merge kernel joins them in key order.
@@ -82,42 +81,66 @@ __device__ __forceinline__ long long paged_units(const PagedAttnParams& p, const
   return u * p.Hkv;
 }
 
-// a CTA's stretch [lo, hi) of the line's `total` units, and where it starts:
-// `rem` units into request b.  With fewer units than CTAs only the first
-// `ctas` = total have one each.
+// A CTA's stretch of the line's `total` units, cut into ctas = min(N, total)
+// stretches of q or q + 1 units (the first `more` of them), and the tile and
+// block that it starts with.
 struct PagedRange {
-  int64_t lo, hi, rem, total;
-  int b, ctas;
-  int tiles, tiles0;           // of the call, of the requests before b
+  int64_t total, q, left;      // left: units of this stretch
+  PagedRequest r;              // request b
+  int ctas, more;
+  int b, tile, h, nb, kb0;
+  int ord, tiles;              // number of the tile on the line; tiles of the call
 };
 
+// x / y and the rest; 64-bit division takes hundreds of cycles, and the numbers are nearly always small
+__device__ __forceinline__ int64_t div64(int64_t x, int64_t y, int64_t& rest) {
+  if ((x | y) >> 31 == 0) {
+    const uint32_t d = static_cast<uint32_t>(x) / static_cast<uint32_t>(y);
+    rest = x - static_cast<int64_t>(d) * y;
+    return d;
+  }
+  const int64_t d = x / y;
+  rest = x - d * y;
+  return d;
+}
+
+// CTA whose stretch holds unit u
+__device__ __forceinline__ int paged_holder(const PagedRange& g, int64_t u) {
+  int64_t rest;
+  const int64_t bound = g.more * (g.q + 1);
+  return static_cast<int>(u < bound ? div64(u, g.q + 1, rest) : g.more + div64(u - bound, g.q, rest));
+}
+
 // One pass over the batch by the whole CTA: each thread sums the units of a
-// run of requests, a scan gives their places on the line.
+// run of requests, a scan gives their places on the line, and the thread that
+// finds the stretch's start on its run tells the others.
 template <int ROWS>
 __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int cta, int ctas) {
-  __shared__ long long warp_sum[32];
-  __shared__ int warp_tiles[32];
-  __shared__ long long found_rem;
-  __shared__ int found_b, found_tiles;
+  __shared__ long long warp_sum[16];
+  __shared__ int warp_tiles[16];
+  __shared__ PagedRange found;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
   const int per = (p.batch + blockDim.x - 1) / blockDim.x;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
   long long sum = 0;
   int tiles = 0;
+  PagedRequest r{};
   for (int b = b0; b < b1; ++b) {
-    const PagedRequest r = paged_request<ROWS>(p, b);
+    r = paged_request<ROWS>(p, b);
     sum += paged_units<ROWS>(p, r);
     tiles += r.tiles * p.Hkv;
   }
   long long upto = sum;
   int tiles_upto = tiles;
+  if (__any_sync(0xffffffffu, sum > 0)) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long x = __shfl_up_sync(0xffffffffu, upto, o);
-    const int y = __shfl_up_sync(0xffffffffu, tiles_upto, o);
-    if (lane >= o) {
-      upto += x;
-      tiles_upto += y;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(0xffffffffu, upto, o);
+      const int y = __shfl_up_sync(0xffffffffu, tiles_upto, o);
+      if (lane >= o) {
+        upto += x;
+        tiles_upto += y;
+      }
     }
   }
   if (lane == 31) {
@@ -128,40 +151,54 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int 
   long long total = 0, before = 0;
   int tiles_all = 0, tiles_before = 0;
   for (int w = 0; w < warps; ++w) {
-    if (w < warp) {
-      before += warp_sum[w];
-      tiles_before += warp_tiles[w];
+    if (w == warp) {
+      before = total;
+      tiles_before = tiles_all;
     }
     total += warp_sum[w];
     tiles_all += warp_tiles[w];
   }
-  PagedRange g;
+  PagedRange g{};
   g.total = total;
   g.tiles = tiles_all;
   g.ctas = static_cast<int>(min64(ctas, total));
-  g.lo = cta < g.ctas ? total * cta / g.ctas : total;
-  g.hi = cta < g.ctas ? total * (cta + 1) / g.ctas : total;
+  if (cta >= g.ctas) return g;   // nothing to do (left = 0)
+  int64_t rest;
+  g.q = div64(total, g.ctas, rest);
+  g.more = static_cast<int>(rest);
+  g.left = g.q + (cta < g.more);
+  const int64_t lo = g.q * cta + min(cta, g.more);
   long long at = before + upto - sum;
-  int tiles_at = tiles_before + tiles_upto - tiles;
-  if (g.lo < g.hi && g.lo >= at && g.lo < at + sum) {
-    for (int b = b0; b < b1; ++b) {
-      const PagedRequest r = paged_request<ROWS>(p, b);
-      const long long u = paged_units<ROWS>(p, r);
-      if (g.lo < at + u) {
-        found_b = b;
-        found_rem = g.lo - at;
-        found_tiles = tiles_at;
-        break;
+  if (lo >= at && lo < at + sum) {
+    int tiles_at = tiles_before + tiles_upto - tiles, b = b0;
+    if (per > 1) {
+      for (;; ++b) {
+        r = paged_request<ROWS>(p, b);
+        const long long u = paged_units<ROWS>(p, r);
+        if (lo < at + u) break;
+        at += u;
+        tiles_at += r.tiles * p.Hkv;
       }
-      at += u;
-      tiles_at += r.tiles * p.Hkv;
     }
+    int64_t x = lo - at;         // units into request b
+    g.r = r;
+    g.b = b;
+    g.nb = paged_blocks<ROWS>(p, r, 0);
+    if (!p.causal) {
+      g.tile = static_cast<int>(div64(x, static_cast<int64_t>(g.nb) * p.Hkv, x));
+    } else {
+      while (x >= static_cast<int64_t>(g.nb) * p.Hkv) {
+        x -= static_cast<int64_t>(g.nb) * p.Hkv;
+        g.nb = paged_blocks<ROWS>(p, r, ++g.tile);
+      }
+    }
+    g.h = static_cast<int>(div64(x, g.nb, x));
+    g.kb0 = static_cast<int>(x);
+    g.ord = tiles_at + g.tile * p.Hkv + g.h;
+    found = g;
   }
   __syncthreads();
-  g.b = g.lo < g.hi ? found_b : p.batch;
-  g.rem = found_rem;
-  g.tiles0 = found_tiles;
-  return g;
+  return found;
 }
 
 // Walks the tiles of a stretch: the key blocks [kb0, kb1) of the nb of row
@@ -173,27 +210,9 @@ struct PagedWalk {
   int b, tile, h, nb, kb0, kb1;
   int ord;                     // number of the tile on the line
 
-  __device__ __forceinline__ PagedWalk(const PagedAttnParams& p, const PagedRange& g) : left(g.hi - g.lo), b(g.b) {
-    if (left <= 0) return;
-    r = paged_request<ROWS>(p, b);
-    tile = 0;
-    nb = paged_blocks<ROWS>(p, r, 0);
-    int64_t rem = g.rem;
-    if (!p.causal) {
-      const int64_t per_tile = static_cast<int64_t>(nb) * p.Hkv;
-      tile = static_cast<int>(rem / per_tile);
-      rem %= per_tile;
-    } else {
-      while (rem >= static_cast<int64_t>(nb) * p.Hkv && tile + 1 < r.tiles) {
-        rem -= static_cast<int64_t>(nb) * p.Hkv;
-        nb = paged_blocks<ROWS>(p, r, ++tile);
-      }
-    }
-    h = static_cast<int>(rem / nb);
-    ord = g.tiles0 + tile * p.Hkv + h;
-    kb0 = static_cast<int>(rem % nb);
-    kb1 = static_cast<int>(min64(nb, kb0 + left));
-  }
+  __device__ __forceinline__ explicit PagedWalk(const PagedRange& g)
+      : r(g.r), left(g.left), b(g.b), tile(g.tile), h(g.h), nb(g.nb), kb0(g.kb0),
+        kb1(static_cast<int>(min64(g.nb, g.kb0 + g.left))), ord(g.ord) {}
   __device__ __forceinline__ bool more() const { return left > 0; }
   __device__ __forceinline__ bool whole() const { return kb0 == 0 && kb1 == nb; }
   __device__ __forceinline__ void next(const PagedAttnParams& p) {
@@ -220,10 +239,11 @@ struct PagedWalk {
 };
 
 // where column c of row r of a partial slot lies: rows of floats, or for the
-// 256-row tiles (a thread per row) columns of float4
+// 256-row tiles (a warp per 32 rows) [32 rows][D / 4][row] float4
 template <int ROWS, int D>
 __device__ __forceinline__ int64_t paged_part_at(int64_t slot, int r, int c) {
-  return ROWS == 16 ? (slot * ROWS + r) * D + c : ((slot * (D / 4) + c / 4) * ROWS + r) * 4 + c % 4;
+  return ROWS == 16 ? (slot * ROWS + r) * D + c
+                    : (((slot * (ROWS / 32) + r / 32) * (D / 4) + c / 4) * 32 + r % 32) * 4 + c % 4;
 }
 
 // Lists tile number seg of a stretch for the merge kernel, if it begins there:
@@ -243,10 +263,10 @@ __device__ __forceinline__ void paged_list(const PagedAttnParams& p, const Paged
     cut.h = w.h;
     cut.first = blockIdx.x;
     cut.slot = 2 * blockIdx.x + (seg > 0);
-    // the pieces behind this one are the first of each stretch up to the one that holds the tile's last unit,
-    // end - 1: floor(W c / N) <= u is c <= ((u + 1) N - 1) / W
-    const int64_t end = g.hi + (w.nb - w.kb1);
-    cut.last = static_cast<int>((end * g.ctas - 1) / g.total);
+    // the pieces behind this one are the first of each stretch up to the one that holds the tile's last unit
+    const int c = blockIdx.x;
+    const int64_t hi = g.q * (c + 1) + min(c + 1, g.more);
+    cut.last = paged_holder(g, hi + (w.nb - w.kb1) - 1);
   }
   if (w.ord < p.cuts_by_tile) p.cuts[w.ord] = cut;   // more only where cu_rows decreases
 }
@@ -258,6 +278,16 @@ __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint3
                "l"(src), "r"(bytes), "r"(smem_u32(bar))
                : "memory");
 }
+
+// untiled store of `bytes` from shared memory (same rules), tracked by this thread's bulk-async group
+__device__ __forceinline__ void bulk_store(void* dst, const void* smem_src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(smem_src)),
+               "r"(bytes)
+               : "memory");
+}
+
+// wait until every bulk store this thread committed is complete
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 
 __device__ __forceinline__ void ldmatrix_x4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -339,7 +369,7 @@ __device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
   int seg = 0;
   PagedCut cut{};
   cut.tiles = g.tiles;
-  for (PagedWalk<ROWS> w(p, g); w.more(); w.next(p), ++seg) {
+  for (PagedWalk<ROWS> w(g); w.more(); w.next(p), ++seg) {
     paged_list<ROWS>(p, g, w, seg, cut);   // every thread writes the same
     const int live = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
     for (int i = threadIdx.x; i < live * D; i += blockDim.x) {
@@ -407,7 +437,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     int it = 0, seg = 0;
     uint32_t issued = 0, par = 0;
     PagedCut cut{};
-    for (PagedWalk<TOK_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+    for (PagedWalk<TOK_ROWS> w(g); ok && w.more(); w.next(p), ++seg) {
       if (lane == 0) paged_list<TOK_ROWS>(p, g, w, seg, cut);
       const int32_t* tab = p.table + w.b * p.table_stride;
       const int live = min(w.r.n * G - w.tile * TOK_ROWS, TOK_ROWS);

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     int it = 0, seg = 0;
     uint32_t issued = 0, par = 0;
     PagedCut cut{};
-    for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+    for (PagedWalk<CV_ROWS> w(g); ok && w.more(); w.next(p), ++seg) {
       if (!is_k && lane == 0) paged_list<CV_ROWS>(p, g, w, seg, cut);
       const int32_t* tab = p.table + w.b * p.table_stride;
       int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     auto has_rows = [&](const PagedWalk<CV_ROWS>& w) { return w.r.n * G - w.tile * CV_ROWS > q * CV_TILE; };
     bool fetched = false;                    // this tile's queries are on their way
     int j = 0;
-    for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p)) {
+    for (PagedWalk<CV_ROWS> w(g); ok && w.more(); w.next(p)) {
       const int units = __shfl_sync(0xffffffffu, w.kb1 - w.kb0, 0);
       if (!__shfl_sync(0xffffffffu, has_rows(w), 0)) {
         // the other tile's blocks: pass them on
@@ -369,7 +369,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     uint8_t* pdst = smem + C::P_OFF + wg * C::P_BYTES + rloc * 128;
     int j = 0, seg = 0, n_s = 0;                     // units of the stretch, tiles, score tiles read so far
     int turns = 0;                                   // units so far that both tiles had rows in
-    for (PagedWalk<CV_ROWS> w(p, g); ok && w.more(); w.next(p), ++seg) {
+    for (PagedWalk<CV_ROWS> w(g); ok && w.more(); w.next(p), ++seg) {
       const int row0 = w.tile * CV_ROWS, units = w.kb1 - w.kb0;
       if (w.r.n * G - row0 <= wg * CV_TILE) {        // no live row in this tile
         j += units;
@@ -484,33 +484,50 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       const float inv = lsum == 0.f ? 0.f : 1.f / lsum;
       const int64_t row = live ? paged_out_row(p, w.r.t0, r, w.h) : 0;
       const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0);
-      // columns [c0, c0 + N) of the row
-      auto put = [&](int c0, auto& v) {
-        constexpr int N = sizeof(v) / sizeof(float);
-        if (!live) return;
-        if (whole) {
+      if (whole) {
+#pragma unroll 1
+        for (int c0 = 0; c0 < D; c0 += 16) {
+          float v[16];
+          tmem_ld16(o_col + c0, v);
+          if (!live) continue;
           uint4* dst = reinterpret_cast<uint4*>(p.o + row * D + c0);
 #pragma unroll
-          for (int e = 0; e < N; e += 8)
+          for (int e = 0; e < 16; e += 8)
             dst[e / 8] = make_uint4(cvt_bf16x2(v[e] * inv, v[e + 1] * inv), cvt_bf16x2(v[e + 2] * inv, v[e + 3] * inv),
                                     cvt_bf16x2(v[e + 4] * inv, v[e + 5] * inv), cvt_bf16x2(v[e + 6] * inv, v[e + 7] * inv));
-        } else {
-          float4* dst = reinterpret_cast<float4*>(p.part + paged_part_at<CV_ROWS, D>(slot, wg * CV_TILE + rloc, c0));
-#pragma unroll
-          for (int e = 0; e < N; e += 4) dst[e / 4 * CV_ROWS] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
         }
-      };
+      } else {
+        // A warp's 32 rows go out in bulk copies of 32 columns through its rows of the P buffer, which is free now.
+        float4* stage = reinterpret_cast<float4*>(smem + C::P_OFF + wg * C::P_BYTES + quarter * 4096) + lane;
+        float* dst = p.part + paged_part_at<CV_ROWS, D>(slot, wg * CV_TILE + quarter * 32, 0);
 #pragma unroll 1
-      for (int c0 = 0; c0 + 64 <= D; c0 += 64) {
-        float v[64];
-        tmem_ld64(o_col + c0, v);
-        put(c0, v);
-      }
+        for (int c0 = 0; c0 < D; c0 += 32) {
+          const bool wide = c0 + 32 <= D;      // D is a multiple of 16
+          if (lane == 0) bulk_wait_read_all();
+          __syncwarp();
+          auto put = [&](auto& v) {
+            constexpr int N = sizeof(v) / sizeof(float);
 #pragma unroll
-      for (int c0 = D / 64 * 64; c0 < D; c0 += 16) {
-        float v[16];
-        tmem_ld16(o_col + c0, v);
-        put(c0, v);
+            for (int e = 0; e < N; e += 4) stage[e / 4 * 32] = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+          };
+          if (wide) {
+            float v[32];
+            tmem_ld32(o_col + c0, v);
+            put(v);
+          } else {
+            float v[16];
+            tmem_ld16(o_col + c0, v);
+            put(v);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            bulk_store(dst + c0 * 32, stage, (wide ? 32 : 16) * 128);
+            bulk_commit_group();
+          }
+        }
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
       }
       tc_fence_before();
       __syncwarp();
@@ -522,6 +539,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
           p.lse[row] = lsum == 0.f ? -INFINITY : (mref + log2f(lsum)) * 0.69314718055994531f;
       }
     }
+    if (lane == 0) bulk_wait_all();
     if (!ok) *abort_flag = 1;
   }
   tc_fence_before();
