@@ -12,6 +12,14 @@
 
 namespace dg {
 
+// Every kernel here may start while the one before it in the stream still
+// runs (programmatic dependent launch): it lets the next one start at once,
+// sets itself up, and waits for the one before it, all of it, ahead of its
+// first access to global memory.  A CTA that leaves early has waited too, so
+// the end of a kernel is the end of everything before it.
+__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ int64_t min64(int64_t a, int64_t b) { return a < b ? a : b; }
 __device__ __forceinline__ int64_t max64(int64_t a, int64_t b) { return a > b ? a : b; }
 
@@ -73,6 +81,8 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
   __shared__ long long red[7][PLAN_THREADS / 32];
   const int b0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.batch / gridDim.x);
   const int b1 = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * p.batch / gridDim.x);
+  pdl_launch_dependents();
+  pdl_wait();
   // sums before b0 (rows, grow, back), over the batch (rows, grow, back), bad bits
   long long v[7] = {0, 0, 0, 0, 0, 0, 0};
   for (int b = threadIdx.x; b < p.batch; b += PLAN_THREADS) {
@@ -200,6 +210,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
   static_assert(HALF % 8 == 0, "16-byte halves");
   const int heads = p.Hq + 2 * p.Hkv, groups = (heads + APPEND_HEADS - 1) / APPEND_HEADS;
   const int64_t it = static_cast<int64_t>(blockIdx.x) * APPEND_THREADS + threadIdx.x;
+  pdl_launch_dependents();
+  pdl_wait();
   if (it >= static_cast<int64_t>(p.rows) * groups * C) return;
   const int c = static_cast<int>(it % C);
   const int h0 = static_cast<int>(it / C % groups) * APPEND_HEADS;

@@ -32,19 +32,18 @@ dg_status check_heads(int Hq, int Hkv, int D) {
 // a launch's own status; an error that the caller left pending is neither
 // reported nor cleared
 template <typename P>
-dg_status paged_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p,
-                       bool overlap = false) {
+dg_status paged_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, void* stream, const P& p) {
   cudaLaunchConfig_t lc{};
   lc.gridDim = grid;
   lc.blockDim = dim3(threads);
   lc.dynamicSmemBytes = smem;
   lc.stream = static_cast<cudaStream_t>(stream);
-  // start while the kernel before it still runs (the kernel waits for its end itself)
+  // it may start while the kernel before it still runs, and waits for its end itself
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   lc.attrs = &attr;
-  lc.numAttrs = overlap ? 1 : 0;
+  lc.numAttrs = 1;
   return cudaLaunchKernelEx(&lc, kernel, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
 }
 
@@ -143,7 +142,7 @@ template <int ROWS, int D>
 dg_status launch_merge(const PagedAttnParams& p, int tiles, int sms, void* stream) {
   using C = MergeCfg<ROWS>;
   const dim3 grid(p.cuts_by_tile ? tiles : sms, ROWS == TOK_ROWS ? 1 : D / 4 / C::COLS);
-  return paged_launch(paged_merge_kernel<ROWS, D>, grid, C::THREADS, 0, stream, p, true);
+  return paged_launch(paged_merge_kernel<ROWS, D>, grid, C::THREADS, 0, stream, p);
 }
 
 template <int D>

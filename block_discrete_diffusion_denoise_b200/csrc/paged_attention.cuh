@@ -310,9 +310,6 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // ----------------------------------------------------------------------------
 // Few rows per request (single tokens): tiles of 16 packed rows (row = i * G +
 // query head of the group), so that the G heads of a group share one read of
@@ -406,6 +403,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
   static_assert(C::STAGES * sizeof(TokDesc) <= 512 && (2 * C::STAGES + 2) * 8 <= 256, "tail layout");
   static_assert(TOK_WARPS * TOK_ROWS * sizeof(float2) == 512, "tail layout");
 
+  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&p.k_map);
@@ -419,7 +417,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     *abort_flag = 0;
     fence_mbar_init();
   }
-  pdl_launch_dependents();
+  pdl_wait();
   const PagedRange g = paged_range<TOK_ROWS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
   const int G = p.Hq / p.Hkv;
   bool ok = true;
@@ -677,7 +675,6 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
 // over a tile's pieces, in one pass with a running maximum.  Bound by the
 // latency of its loads, of which each thread keeps several in flight; a small
 // tile's pieces are dealt out to groups of threads, joined in shared memory.
-// Launched while the attention kernel still runs.
 // ----------------------------------------------------------------------------
 template <int ROWS>
 struct MergeCfg {
@@ -715,6 +712,7 @@ __global__ void __launch_bounds__(MergeCfg<ROWS>::THREADS) paged_merge_kernel(co
   using C = MergeCfg<ROWS>;
   __shared__ float4 s_o[ROWS == 16 ? C::THREADS : 1];
   __shared__ float2 s_ml[ROWS == 16 ? C::THREADS : 1];
+  pdl_launch_dependents();
   pdl_wait();
   // by tile, the first entry says how many there are
   if (p.cuts_by_tile && static_cast<int>(blockIdx.x) >= p.cuts[0].tiles) return;

@@ -159,6 +159,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   static_assert((2 + 4 * C::STAGES + 20) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
   static_assert(CV_MASKS >= C::STAGES + 4, "a mask is read before its slot comes round");
 
+  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&p.k_map);
@@ -187,8 +188,8 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     tmem_alloc(tmem_holder, C::TMEM_COLS);
     tmem_relinquish();
   }
-  pdl_launch_dependents();
   tc_fence_before();
+  pdl_wait();
   const PagedRange g = paged_range<CV_ROWS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
