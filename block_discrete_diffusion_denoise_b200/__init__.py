@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("DG_LIBRARY", os.path.join(HERE, "libdg.so"))
@@ -135,8 +136,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dg_lmhead_argmax_static": ([P, I32, I32, P, I32, F32, P, P, P, P], I32),
         "dg_paged_plan": ([P, P, I32, P, I32, I64, P, I32, P, I32, P, P, P, P, I32, P, P], I32),
         "dg_paged_append": ([P, I64, I32, I32, I32, I32, P, P, P, I32, P, P, I32, I32, P, P], I32),
-        "dg_paged_attention_workspace": ([ctypes.POINTER(dg_paged_attention_args), ctypes.POINTER(I64)], I32),
-        "dg_paged_attention": ([ctypes.POINTER(dg_paged_attention_args), P], I32),
+        # dg_paged_attention_args by address: byref() of the struct, or its bytes
+        "dg_paged_attention_workspace": ([P, ctypes.POINTER(I64)], I32),
+        "dg_paged_attention": ([P, P], I32),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -153,6 +155,7 @@ def _ptr(t) -> int | None:
 
 
 DG_ERR_INVALID_ARG = 1
+DG_ERR_UNSUPPORTED = 7
 
 
 def _invalid(msg: str):
@@ -476,48 +479,65 @@ def lmhead_argmax_static(z, embed, temperature, argmax=None, lse=None, conf=None
 
 # --- paged KV cache ---
 # Context-free calls on torch CUDA tensors.  They run on torch's current stream
-# of the tensors' device, allocate nothing and synchronise nothing; arguments
-# are checked first, and a bad one raises DGError with nothing launched.
+# of the tensors' device, synchronise nothing, and allocate at most the
+# workspace of an attention call; arguments are checked first, and a bad one
+# raises DGError with nothing launched.
+#
+# A call's host time counts (its kernels take a few microseconds), so a good
+# operand is told by four attribute reads and the messages are made for a bad
+# one only.
 
-def _paged_dev(t, dtype, ndim, what, dev=None):
-    """t as an operand: a CUDA tensor of `dtype` with `ndim` dimensions, the
-    last one dense, on `dev` (the first operand's device)."""
-    import torch
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or t.dim() != ndim:
-        _invalid(f"{what}: expected a {ndim}-dimensional CUDA tensor of {dtype}, got "
-                 f"{getattr(t, 'dtype', type(t).__name__)} {tuple(getattr(t, 'shape', ()))} on "
-                 f"{getattr(t, 'device', '?')}")
-    if dev is not None and t.device != dev:
-        _invalid(f"{what}: on {t.device}, the other tensors are on {dev}")
-    return t
+def _paged_bad(t, what, want):
+    got = f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ' (strided)'}" \
+        if hasattr(t, "is_contiguous") else type(t).__name__
+    _invalid(f"{what}: expected {want}, got {got}")
 
 
-def _paged_flat(t, dtype, n, what, dev):
-    _paged_dev(t, dtype, 1, what, dev)
-    if t.numel() < n or not t.is_contiguous():
-        _invalid(f"{what}: {t.numel()} elements{'' if t.is_contiguous() else ' (strided)'}, the call needs {n}")
-    return t.data_ptr()
+def _paged_ints(t, n, what, i32, idx):
+    """Address of t: a contiguous int32 tensor of at least n elements on CUDA device idx."""
+    try:
+        if t.dtype is i32 and t.get_device() == idx and t.numel() >= n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _paged_bad(t, what, f"a contiguous int32 tensor of at least {n} elements on cuda:{idx}")
 
 
-def _paged_pools(k_pages, v_pages, dev):
-    import torch
+def _paged_operand(t, dtype, ndim, what):
+    """CUDA device index of t, a tensor of `dtype` with `ndim` dimensions."""
+    idx = t.get_device() if hasattr(t, "get_device") else -1
+    if idx < 0 or t.dtype is not dtype or t.dim() != ndim:
+        _paged_bad(t, what, f"a {ndim}-dimensional CUDA tensor of {dtype}")
+    return idx
+
+
+def _paged_table(t, i32, idx):
+    """(batch, width, row stride) of a block table on CUDA device idx (None: its own)."""
+    own = _paged_operand(t, i32, 2, "block_table")
+    B, W = t.shape
+    if (idx is not None and own != idx) or W < 1 or (t.stride(1) != 1 and W > 1):
+        _paged_bad(t, "block_table", f"a [batch, width] int32 tensor with adjacent entries on cuda:{idx}")
+    return B, W, (t.stride(0) if B > 1 else W)
+
+
+def _paged_pools(k_pages, v_pages, bf16, idx):
     for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        _paged_dev(t, torch.bfloat16, 4, what, dev)
-        if not t.is_contiguous():
-            _invalid(f"{what}: strided")
-    if k_pages.shape != v_pages.shape:
-        _invalid(f"k_pages {tuple(k_pages.shape)} and v_pages {tuple(v_pages.shape)} differ")
-    return k_pages.shape                          # n_pages, n_kv_heads, page_size, head_dim
+        if _paged_operand(t, bf16, 4, what) != idx or not t.is_contiguous():
+            _paged_bad(t, what, f"a contiguous [n_pages, n_kv_heads, page_size, head_dim] bf16 tensor on cuda:{idx}")
+    shape = k_pages.shape
+    if shape != v_pages.shape:
+        _invalid(f"k_pages {tuple(shape)} and v_pages {tuple(v_pages.shape)} differ")
+    return shape
 
 
-def _paged_call(name, dev, *args, stream=True):
-    """The call on torch's current stream of `dev`, with that device current."""
+def _paged_call(name, idx, *args):
+    """The call with CUDA device idx current, its stream torch's current one there."""
     import torch
-    f = getattr(load_library(), name)
-    if torch.cuda.current_device() != dev.index:
-        with torch.cuda.device(dev):
-            return _paged_call(name, dev, *args, stream=stream)
-    st = f(*args, torch.cuda.current_stream().cuda_stream) if stream else f(*args)
+    c = torch._C                      # torch.cuda.current_stream() makes an object of what these two tell
+    if c._cuda_getDevice() != idx:
+        with torch.cuda.device(idx):
+            return _paged_call(name, idx, *args)
+    st = getattr(_lib or load_library(), name)(*args, c._cuda_getCurrentRawStream(idx))
     if st != DG_OK:
         raise DGError(st, f"{name} refused (shape, alignment or capacity; see include/dg.h)")
 
@@ -542,21 +562,19 @@ def paged_plan(cached_lens, new_rows, block_table, free_pages, free_state, page_
     call's free_state_out, and another buffer to write)."""
     import torch
     i32 = torch.int32
-    dev = _paged_dev(block_table, i32, 2, "block_table").device
-    B, W = block_table.shape
-    if block_table.stride(1) != 1:
-        _invalid("block_table: entries of a row must be adjacent")
-    _paged_dev(free_pages, i32, 1, "free_pages", dev)
-    _paged_dev(slots, i32, 1, "slots", dev)
-    n_pages, cap = free_pages.numel(), slots.numel()
-    _paged_call("dg_paged_plan", dev,
-                _paged_flat(cached_lens, i32, B, "cached_lens", dev), _paged_flat(new_rows, i32, B, "new_rows", dev),
-                B, block_table.data_ptr(), W, block_table.stride(0) if B > 1 else W,
-                _paged_flat(free_pages, i32, 1, "free_pages", dev), n_pages,
-                _paged_flat(free_state, i32, 2, "free_state", dev), int(page_size),
-                _paged_flat(cu_rows, i32, B + 1, "cu_rows", dev), _paged_flat(kv_lens, i32, B, "kv_lens", dev),
-                _paged_flat(positions, i32, cap, "positions", dev), _paged_flat(slots, i32, cap, "slots", dev), cap,
-                _paged_flat(free_state_out, i32, 4, "free_state_out", dev))
+    idx = _paged_operand(block_table, i32, 2, "block_table")
+    B, W, stride = _paged_table(block_table, i32, idx)
+    ring = _paged_ints(free_pages, 1, "free_pages", i32, idx)
+    rows = _paged_ints(slots, 0, "slots", i32, idx)
+    cap = slots.numel()
+    if B == 0:
+        _invalid("block_table: no request")
+    _paged_call("dg_paged_plan", idx, _paged_ints(cached_lens, B, "cached_lens", i32, idx),
+                _paged_ints(new_rows, B, "new_rows", i32, idx), B, block_table.data_ptr(), W, stride, ring,
+                free_pages.numel(), _paged_ints(free_state, 2, "free_state", i32, idx), page_size,
+                _paged_ints(cu_rows, B + 1, "cu_rows", i32, idx), _paged_ints(kv_lens, B, "kv_lens", i32, idx),
+                _paged_ints(positions, cap, "positions", i32, idx), rows, cap,
+                _paged_ints(free_state_out, 4, "free_state_out", i32, idx))
 
 
 def paged_append(qkv, positions, slots, rope, k_pages, v_pages, q_out):
@@ -566,24 +584,31 @@ def paged_append(qkv, positions, slots, rope, k_pages, v_pages, q_out):
     D].  positions and slots (int32) hold at least `rows` entries; rope is
     rope_table's."""
     import torch
-    dev = _paged_dev(qkv, torch.bfloat16, 2, "qkv").device
-    rows = qkv.shape[0]
-    n_pages, hkv, page, d = _paged_pools(k_pages, v_pages, dev)
-    _paged_dev(q_out, torch.bfloat16, 3, "q_out", dev)
-    hq = q_out.shape[1]
-    if q_out.shape != (rows, hq, d) or not q_out.is_contiguous():
-        _invalid(f"q_out: expected a contiguous [{rows}, Hq, {d}] tensor, got {tuple(q_out.shape)}")
-    if qkv.shape[1] != (hq + 2 * hkv) * d or (qkv.stride(1) != 1 and rows):
-        _invalid(f"qkv: expected rows of {(hq + 2 * hkv) * d} adjacent elements, got {tuple(qkv.shape)}")
-    _paged_dev(rope, torch.float32, 3, "rope", dev)
-    if rope.shape[1:] != (d // 2, 2) or not rope.is_contiguous():
-        _invalid(f"rope: expected a contiguous [positions, {d // 2}, 2] tensor, got {tuple(rope.shape)}")
+    bf16, i32 = torch.bfloat16, torch.int32
+    idx = _paged_operand(qkv, bf16, 2, "qkv")
+    rows, width = qkv.shape
+    n_pages, hkv, page, d = _paged_pools(k_pages, v_pages, bf16, idx)
+    if _paged_operand(q_out, bf16, 3, "q_out") != idx or not q_out.is_contiguous():
+        _paged_bad(q_out, "q_out", f"a contiguous [{rows}, Hq, {d}] bf16 tensor on cuda:{idx}")
+    n, hq, dq = q_out.shape
+    if n != rows or dq != d:
+        _paged_bad(q_out, "q_out", f"a contiguous [{rows}, Hq, {d}] bf16 tensor on cuda:{idx}")
+    if width != (hq + 2 * hkv) * d or (qkv.stride(1) != 1 and rows):
+        _paged_bad(qkv, "qkv", f"rows of {(hq + 2 * hkv) * d} adjacent elements")
+    if _paged_operand(rope, torch.float32, 3, "rope") != idx or not rope.is_contiguous() \
+            or rope.shape[1:] != (d // 2, 2):
+        _paged_bad(rope, "rope", f"a contiguous [positions, {d // 2}, 2] float32 tensor on cuda:{idx}")
+    pos = _paged_ints(positions, rows, "positions", i32, idx)
+    at = _paged_ints(slots, rows, "slots", i32, idx)
     if rows == 0:
         return
-    _paged_call("dg_paged_append", dev, qkv.data_ptr(), qkv.stride(0) if rows > 1 else qkv.shape[1], rows, hq, hkv, d,
-                _paged_flat(positions, torch.int32, rows, "positions", dev),
-                _paged_flat(slots, torch.int32, rows, "slots", dev), rope.data_ptr(), rope.shape[0],
-                k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page, q_out.data_ptr())
+    _paged_call("dg_paged_append", idx, qkv.data_ptr(), qkv.stride(0) if rows > 1 else width, rows, hq, hkv, d, pos,
+                at, rope.data_ptr(), rope.shape[0], k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page,
+                q_out.data_ptr())
+
+
+_PAGED_ATTENTION_ARGS = struct.Struct("@9P3q10if4x")     # dg_paged_attention_args
+_paged_workspace_bytes: dict = {}                        # (device, head_dim, group, bound of rows): bytes
 
 
 def paged_attention(q, k_pages, v_pages, block_table, kv_lens, cu_rows, out, lse=None, causal=False, max_rows=0,
@@ -597,36 +622,45 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_lens, cu_rows, out, lse
     upper bound of a request's rows where the caller knows one (it picks the
     kernel); scale defaults to D ** -0.5."""
     import torch
-    dev = _paged_dev(q, torch.bfloat16, 3, "q").device
-    rows, hq, d = q.shape
-    n_pages, hkv, page, dk = _paged_pools(k_pages, v_pages, dev)
+    bf16, i32 = torch.bfloat16, torch.int32
+    idx = _paged_operand(q, bf16, 3, "q")
+    shape = q.shape
+    rows, hq, d = shape
+    n_pages, hkv, page, dk = _paged_pools(k_pages, v_pages, bf16, idx)
     if dk != d or (rows and (q.stride(2) != 1 or q.stride(1) != d)):
-        _invalid(f"q: expected [rows, Hq, {dk}] with adjacent heads, got {tuple(q.shape)}")
-    _paged_dev(out, torch.bfloat16, 3, "out", dev)
-    if out.shape != q.shape or not out.is_contiguous():
-        _invalid(f"out: expected a contiguous {tuple(q.shape)} tensor, got {tuple(out.shape)}")
+        _paged_bad(q, "q", f"[rows, Hq, {dk}] with adjacent heads")
+    if _paged_operand(out, bf16, 3, "out") != idx or out.shape != shape or not out.is_contiguous():
+        _paged_bad(out, "out", f"a contiguous {tuple(shape)} bf16 tensor on cuda:{idx}")
+    lse_at = 0
     if lse is not None:
-        _paged_dev(lse, torch.float32, 2, "lse", dev)
-        if lse.shape != (rows, hq) or not lse.is_contiguous():
-            _invalid(f"lse: expected a contiguous {(rows, hq)} tensor, got {tuple(lse.shape)}")
-    _paged_dev(block_table, torch.int32, 2, "block_table", dev)
-    B, W = block_table.shape
-    if block_table.stride(1) != 1 and W > 1:
-        _invalid("block_table: entries of a row must be adjacent")
+        if _paged_operand(lse, torch.float32, 2, "lse") != idx or lse.shape != (rows, hq) or not lse.is_contiguous():
+            _paged_bad(lse, "lse", f"a contiguous {(rows, hq)} float32 tensor on cuda:{idx}")
+        lse_at = lse.data_ptr()
+    B, W, stride = _paged_table(block_table, i32, idx)
+    kv = _paged_ints(kv_lens, B, "kv_lens", i32, idx)
+    cu = _paged_ints(cu_rows, B + 1, "cu_rows", i32, idx)
     if rows == 0 or B == 0:
         return
-    a = dg_paged_attention_args(
-        q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(),
-        _paged_flat(kv_lens, torch.int32, B, "kv_lens", dev), _paged_flat(cu_rows, torch.int32, B + 1, "cu_rows", dev),
-        out.data_ptr(), None if lse is None else lse.data_ptr(), None, 0, q.stride(0) if rows > 1 else hq * d,
-        block_table.stride(0) if B > 1 else W, rows, B, hq, hkv, d, n_pages, page, W, 1 if causal else 0,
-        int(max_rows), d ** -0.5 if scale is None else float(scale))
-    need = ctypes.c_int64()
-    _paged_call("dg_paged_attention_workspace", dev, ctypes.byref(a), ctypes.byref(need), stream=False)
+    max_rows = int(max_rows)
+    if hq % hkv:
+        raise DGError(DG_ERR_UNSUPPORTED, f"{hq} query heads on {hkv} kv heads")
+    head = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), kv, cu, out.data_ptr(), lse_at)
+    tail = (q.stride(0) if rows > 1 else hq * d, stride, rows, B, hq, hkv, d, n_pages, page, W, 1 if causal else 0,
+            max_rows, d ** -0.5 if scale is None else scale)
+    # its size goes by the device and these numbers alone, and all bounds of over 16 rows are alike
+    key = (idx, d, hq // hkv, min(max_rows if 0 < max_rows < rows else rows, 17))
+    need = _paged_workspace_bytes.get(key)
+    if need is None:
+        n = ctypes.c_int64()
+        with torch.cuda.device(idx):
+            st = load_library().dg_paged_attention_workspace(_PAGED_ATTENTION_ARGS.pack(*head, 0, 0, *tail),
+                                                             ctypes.byref(n))
+        if st != DG_OK:
+            raise DGError(st, "dg_paged_attention refused (shape, alignment or capacity; see include/dg.h)")
+        need = _paged_workspace_bytes[key] = n.value
     # from torch's allocator: calls on other streams and in other graphs get memory of their own
-    ws = torch.empty(need.value, dtype=torch.uint8, device=dev)
-    a.workspace, a.workspace_bytes = ws.data_ptr(), need.value
-    _paged_call("dg_paged_attention", dev, ctypes.byref(a))
+    ws = q.new_empty(need // 2)
+    _paged_call("dg_paged_attention", idx, _PAGED_ATTENTION_ARGS.pack(*head, ws.data_ptr(), need, *tail))
 
 
 def anneal_temperature(step: int, max_steps: int = 48, t_first: float = 0.8, t_last: float = 0.4) -> float:

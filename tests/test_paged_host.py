@@ -22,6 +22,16 @@ def test_argument_struct_matches_the_header():
     assert want == list(dg.dg_paged_attention_args._fields_)
 
 
+def test_packed_arguments_match_the_struct():
+    """the binding packs dg_paged_attention_args without building the ctypes object"""
+    fields = dg.dg_paged_attention_args._fields_
+    values = list(range(1, len(fields))) + [0.5]
+    packed = dg._PAGED_ATTENTION_ARGS.pack(*values)
+    assert len(packed) == ctypes.sizeof(dg.dg_paged_attention_args)
+    s = dg.dg_paged_attention_args.from_buffer_copy(packed)
+    assert [getattr(s, n) for n, _ in fields] == values
+
+
 def plan(**kw):
     a = dict(cached=A, new=A + 0x1000, batch=3, table=A + 0x2000, width=8, stride=8, ring=A + 0x3000, n_pages=100,
              state=A + 0x4000, page=64, cu=A + 0x5000, kv=A + 0x6000, pos=A + 0x7000, slots=A + 0x8000, cap=10,
