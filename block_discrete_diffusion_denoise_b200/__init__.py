@@ -30,7 +30,7 @@ EXPORTS = ["dg_create", "dg_destroy", "dg_prefill", "dg_denoise_step", "dg_denoi
            "dg_debug_gemm", "dg_debug_profile",
            "dg_debug_profile_read", "dg_debug_launch_count", "dg_debug_timeline_reset", "dg_debug_timeline",
            "dg_lmhead_argmax_static", "dg_paged_plan", "dg_paged_append",
-           "dg_paged_attention_workspace", "dg_paged_attention"]
+           "dg_paged_attention_workspace", "dg_paged_attention", "dg_prefill_ragged", "dg_cached_lens"]
 
 # kernel ids of the timeline records (DG_K_* in dg.h)
 TIMELINE_KERNELS = {10: "gemm_dense", 11: "gemm_moe", 13: "gemm_lmhead", 20: "attention", 21: "attn_merge", 30: "route_dispatch",
@@ -108,6 +108,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dg_create": ([ctypes.POINTER(dg_config), ctypes.POINTER(dg_weights), P, ctypes.POINTER(P)], I32),
         "dg_destroy": ([P], I32),
         "dg_prefill": ([P, P, I32, I32], I32),
+        "dg_prefill_ragged": ([P, P, I32, P], I32),
+        "dg_cached_lens": ([P, P], I32),
         "dg_denoise_step": ([P, P, I32, U64, F32, P, P, P], I32),
         "dg_denoise_step_host": ([P, P, I32, U64, F32, P, P, P], I32),
         "dg_denoise_step_entropy": ([P, P, I32, U64, ctypes.POINTER(dg_entropy_args), P, P, P, P, P], I32),
@@ -313,6 +315,19 @@ class Context:
         self._check(self.lib.dg_prefill(self.ctx, self._dev(tokens, torch.int32, B * P, "tokens"), B, P))
         self._batch = int(B)
 
+    def prefill_ragged(self, tokens, lens):
+        """Prompts of different lengths: `tokens` is a one-dimensional int32
+        tensor with the prompts one behind another, `lens` their lengths
+        (host numbers).  The steps and commit_block then work on canvases
+        [len(lens), canvas] as after prefill."""
+        import torch
+        lens = [int(n) for n in lens]
+        if getattr(tokens, "dim", lambda: 0)() != 1 or not lens or min(lens) < 1:
+            _invalid("prefill_ragged: tokens must be a [sum of lens] tensor, every length at least 1")
+        self._check(self.lib.dg_prefill_ragged(self.ctx, self._dev(tokens, torch.int32, sum(lens), "tokens"),
+                                               len(lens), (ctypes.c_int32 * len(lens))(*lens)))
+        self._batch = len(lens)
+
     def denoise_step(self, canvas_in, step, seed, tau, canvas_out, conf, settled=None):
         import torch
         n, B = self._n(), self._batch or 0
@@ -360,6 +375,14 @@ class Context:
     @property
     def cached_len(self) -> int:
         return self.lib.dg_cached_len(self.ctx)
+
+    @property
+    def cached_lens(self) -> list:
+        """Committed length of every sequence of the last prefill."""
+        n = (ctypes.c_int32 * (self._batch or 0))()
+        if self._batch:
+            self._check(self.lib.dg_cached_lens(self.ctx, n))
+        return list(n)
 
     # --- test hooks ---
     def debug_capture(self, enable: bool):
@@ -676,7 +699,8 @@ def generate_blocks(ctx: Context, prefix, init_canvas, n_blocks: int, max_steps:
                     commit_last: bool = False, before_step=None, after_step=None, entropy=None) -> dict:
     """Block-autoregressive generation through the C ABI (codemajin.net
     "DiffusionGemma architecture", section 3.2, block-AR; aibars.net, block
-    commit): prefill the prompt causally, then for each block start from
+    commit): prefill the prompt causally (prefix [batch, length], or a list of
+    int32 tensors of different lengths), then for each block start from
     init_canvas(k) (an int32 CUDA tensor [batch, canvas], e.g. uniform noise),
     run up to max_steps denoising steps, stop as soon as every position of
     every sequence is settled (conf >= tau, read from the all-settled flags),
@@ -698,8 +722,12 @@ def generate_blocks(ctx: Context, prefix, init_canvas, n_blocks: int, max_steps:
     Returns {"blocks": [final canvas of each block], "steps": [steps taken per
     block], "settled": [whether each block stopped early]}."""
     import torch
-    B, C = int(prefix.shape[0]), int(ctx.cfg["canvas"])
-    ctx.prefill(prefix)
+    ragged = isinstance(prefix, (list, tuple))
+    B, C = (len(prefix) if ragged else int(prefix.shape[0])), int(ctx.cfg["canvas"])
+    if ragged:
+        ctx.prefill_ragged(torch.cat([p.reshape(-1) for p in prefix]), [p.numel() for p in prefix])
+    else:
+        ctx.prefill(prefix)
     out = {"blocks": [], "steps": [], "settled": []}
     for k in range(n_blocks):
         cur = init_canvas(k).to(torch.int32).contiguous()

@@ -30,6 +30,9 @@ struct LayerMaps {
   CUtensorMap kc, vc;  // this layer's K / V cache rows, 64 x 64 boxes
 };
 
+// pages of a ragged batch's cache: one TMA box of 64 positions
+constexpr int kRaggedShift = 6, kRaggedPage = 1 << kRaggedShift;
+
 // the sampler that ends a step
 enum Sampler : int { SAMPLER_TAU = 0, SAMPLER_ENTROPY = 1, SAMPLER_COUNT = 2 };
 
@@ -39,6 +42,7 @@ struct StepGraph {
   cudaGraph_t graph = nullptr;
   cudaGraphExec_t exec = nullptr;
   int B = -1, P = -1;
+  bool ragged = false;             // lengths are read on the device: any P
   cudaGraphNode_t embed_node = nullptr, sample_node = nullptr;
   std::vector<cudaGraphNode_t> lm_nodes;       // LM-head passes (statistics, then probabilities)
   cudaKernelNodeParams embed_kp{}, sample_kp{};
@@ -128,9 +132,26 @@ struct dg_ctx {
   CUtensorMap m_u16{}, m_u64{}, m_u128{}, m_o64{}, m_xp16{}, m_h16{}, m_hs16{}, m_embed{};
   CUtensorMap m_xp64{}, m_h64{}, m_hs64{};         // 64-row boxes (expert GEMM B)
   CUtensorMap m_q4{};  // queries as (D, G, Hkv, token): one GQA group's rows per box
+  // ragged batches (dg_prefill_ragged): this memory's cache as a pool of pages of kRaggedPage positions
+  bool ragged = false;
+  std::vector<int32_t> lens;       // committed length of each sequence
+  void* rg_ws = nullptr;
+  int rg_pages = 0, rg_width = 0;  // pages of a layer's pool, pages a sequence may hold
+  int rg_rows = 0;                 // most new rows of one sequence in the current plan
+  int rg_cur = 0;                  // free_state in use
+  int32_t* rg_lens = nullptr;      // [max_batch] committed lengths (the planned call's cached lengths)
+  int32_t* rg_new = nullptr;       // [max_batch] new rows of the planned call
+  int32_t* rg_table = nullptr;     // [max_batch][rg_width]
+  int32_t* rg_ring = nullptr;      // [rg_pages]
+  int32_t* rg_state = nullptr;     // [2][4]
+  int32_t* rg_cu = nullptr;        // [max_batch + 1]
+  int32_t* rg_kv = nullptr;        // [max_batch]
+  int32_t* rg_pos = nullptr;       // [R]
+  int32_t* rg_slots = nullptr;     // [R]
+  void* rg_attn = nullptr;         // attention workspace
   // state
   int B = 0;
-  int P = 0;
+  int P = 0;                       // committed length (ragged: the longest)
   bool prefilled = false;
   uint64_t wait_limit_ns = 1000000000ull;
   bool trace = false;          // DG_TRACE=1: launch shapes to stderr
@@ -246,6 +267,17 @@ cudaError_t launch(dg_ctx* c, void (*kernel)(KArgs...), dim3 grid, dim3 block, s
   } while (0)
 
 DevErr dev_err(const dg_ctx* c) { return DevErr{c->err_word, c->wait_limit_ns}; }
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+constexpr int kMaxSmemPerCta = 232448;  // dynamic shared memory a CTA may opt into
+constexpr int kMaxDevices = 64;
+
+}  // namespace
+
+#include "paged_api.cuh"
+
+namespace {
 
 // Profiling hook: an event pair around the launches of one kernel class.
 struct ProfScope {
@@ -392,6 +424,92 @@ dg_status attention(dg_ctx* c, int l, int B, int n, int pos0, bool causal) {
   return DG_OK;
 }
 
+// The ragged batch's counterpart of the contiguous RoPE and attention launches,
+// on the rows that the current plan describes.
+dg_status ragged_append(dg_ctx* c, int l, int T, int splits) {
+  const size_t layer_off = static_cast<size_t>(l) * c->cfg.max_batch * c->Hkv * c->cfg.max_seq * c->D;
+  PagedAppendParams p{};
+  p.part = c->part;
+  p.splits = splits;
+  p.positions = c->rg_pos;
+  p.slots = c->rg_slots;
+  p.rope = reinterpret_cast<const float4*>(c->rope);
+  p.k = c->kcache + layer_off;
+  p.v = c->vcache + layer_off;
+  p.q = c->q;
+  p.n_slots = static_cast<int64_t>(c->rg_pages) * kRaggedPage;
+  p.rows = T;
+  p.n_positions = c->cfg.max_seq;
+  p.Hq = c->Hq;
+  p.Hkv = c->Hkv;
+  p.page_shift = kRaggedShift;
+  ProfScope ps(c, DG_PROF_OTHER);
+  const dg_status st = launch_append<true>(p, c->D, c->stream);
+  if (st != DG_OK) return fail(c, st, "ragged append: %s", cudaGetErrorString(cudaGetLastError()));
+  c->launches++;
+  return DG_OK;
+}
+
+dg_status ragged_attention(dg_ctx* c, int l, int T, bool causal) {
+  CanvasParams cp;
+  PagedAttnParams& p = cp.a;
+  p.k_map = c->lmaps[l].kc;
+  p.v_map = c->lmaps[l].vc;
+  cp.q_map = c->m_q4;
+  p.q = c->q;
+  p.q_stride = c->HD;
+  p.table = c->rg_table;
+  p.table_stride = c->rg_width;
+  p.kv_lens = c->rg_kv;
+  p.cu_rows = c->rg_cu;
+  p.o = c->o;
+  p.lse = nullptr;
+  p.rows = T;
+  p.batch = c->B;
+  p.Hq = c->Hq;
+  p.Hkv = c->Hkv;
+  p.n_pages = c->rg_pages;
+  p.page_shift = kRaggedShift;
+  p.width = c->rg_width;
+  p.causal = causal ? 1 : 0;
+  p.scale_log2 = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(c->D)));
+  p.err = dev_err(c);
+  ProfScope ps(c, DG_PROF_ATTENTION);
+  const dg_status st = launch_attention(cp, few_rows(T, c->rg_rows, c->Hq / c->Hkv), c->D, c->rg_attn, c->sms, c->stream);
+  if (st != DG_OK) return fail(c, st, "ragged attention: %s", cudaGetErrorString(cudaGetLastError()));
+  c->launches += 2;
+  return DG_OK;
+}
+
+// Plan the next forward: rows[b] new rows behind each committed length.  The
+// pages it takes are the sequences' once ragged_adopt follows; until then a
+// plan may be made again, or used by any number of steps.
+dg_status ragged_plan(dg_ctx* c, const std::vector<int32_t>& rows) {
+  c->rg_rows = *std::max_element(rows.begin(), rows.end());
+  DG_CUDA(c, cudaMemcpyAsync(c->rg_new, rows.data(), rows.size() * 4, cudaMemcpyHostToDevice, c->stream));
+  const dg_status st = dg_paged_plan(c->rg_lens, c->rg_new, c->B, c->rg_table, c->rg_width, c->rg_width, c->rg_ring,
+                                     c->rg_pages, c->rg_state + 4 * c->rg_cur, kRaggedPage, c->rg_cu, c->rg_kv,
+                                     c->rg_pos, c->rg_slots, c->R, c->rg_state + 4 * (c->rg_cur ^ 1), c->stream);
+  if (st != DG_OK) return fail(c, st, "ragged plan");
+  c->launches++;
+  return DG_OK;
+}
+
+// the planned rows are committed
+dg_status ragged_adopt(dg_ctx* c, const std::vector<int32_t>& rows) {
+  DG_CUDA(c, cudaMemcpyAsync(c->rg_lens, c->rg_kv, c->B * 4, cudaMemcpyDeviceToDevice, c->stream));
+  c->rg_cur ^= 1;
+  for (int b = 0; b < c->B; ++b) c->lens[b] += rows[b];
+  return DG_OK;
+}
+
+// pages that the batch needs with `more` positions behind each of `lens`
+int64_t ragged_pages(const std::vector<int32_t>& lens, int more) {
+  int64_t n = 0;
+  for (int32_t x : lens) n += (x + more + kRaggedPage - 1) / kRaggedPage;
+  return n;
+}
+
 // record: capture the expert choices (denoising steps only: the capture
 // buffers hold R_step rows per layer)
 dg_status moe(dg_ctx* c, int l, int T, bool record) {
@@ -458,6 +576,8 @@ dg_status moe(dg_ctx* c, int l, int T, bool record) {
 //                   to the cache; the last layer stops after its K/V.
 //   causal = false: denoising step; canvas K/V go to cache rows [P, P+C)
 //                   (beyond the committed length), then the LM head runs.
+// In a ragged batch the current plan says where the rows belong, and pos0 is
+// not looked at.
 dg_status forward(dg_ctx* c, const int32_t* tokens, int tok_stride, int tok_off, int B, int n, int pos0,
                   bool causal, int32_t* settled) {
   const int T = B * n;
@@ -475,19 +595,27 @@ dg_status forward(dg_ctx* c, const int32_t* tokens, int tok_stride, int tok_off,
     int s1 = 1;
     dg_status st = gemm_dense(c, lm.wqkv, c->m_u64, c->QKV, T, c->d, &s1);
     if (st != DG_OK) return st;
-    const size_t layer_off = static_cast<size_t>(l) * c->cfg.max_batch * c->Hkv * c->cfg.max_seq * c->D;
-    ProfScope ps9(c, DG_PROF_OTHER);
-    DG_LAUNCH(c, rope_qkv_kernel, dim3(T, ROPE_CTAS_PER_ROW),
-              std::min(ROPE_MAX_THREADS,
-                       (rope_items(c->Hq, c->Hkv, c->D) + ROPE_CTAS_PER_ROW * 32 - 1) / (ROPE_CTAS_PER_ROW * 32) * 32),
-              0,
-              static_cast<const float*>(c->part), s1, T, n, pos0, c->Hq, c->Hkv,
-              c->D, static_cast<const float2*>(c->rope), c->q, c->kcache + layer_off, c->vcache + layer_off,
-              c->cfg.max_seq);
-    ps9.end();
-    if (causal && l == c->L - 1) break;  // only this layer's keys/values feed the cache
-    st = attention(c, l, B, n, pos0, causal);
-    if (st != DG_OK) return st;
+    if (c->ragged) {
+      st = ragged_append(c, l, T, s1);
+      if (st != DG_OK) return st;
+      if (causal && l == c->L - 1) break;
+      st = ragged_attention(c, l, T, causal);
+      if (st != DG_OK) return st;
+    } else {
+      const size_t layer_off = static_cast<size_t>(l) * c->cfg.max_batch * c->Hkv * c->cfg.max_seq * c->D;
+      ProfScope ps9(c, DG_PROF_OTHER);
+      DG_LAUNCH(c, rope_qkv_kernel, dim3(T, ROPE_CTAS_PER_ROW),
+                std::min(ROPE_MAX_THREADS,
+                         (rope_items(c->Hq, c->Hkv, c->D) + ROPE_CTAS_PER_ROW * 32 - 1) / (ROPE_CTAS_PER_ROW * 32) * 32),
+                0,
+                static_cast<const float*>(c->part), s1, T, n, pos0, c->Hq, c->Hkv,
+                c->D, static_cast<const float2*>(c->rope), c->q, c->kcache + layer_off, c->vcache + layer_off,
+                c->cfg.max_seq);
+      ps9.end();
+      if (causal && l == c->L - 1) break;  // only this layer's keys/values feed the cache
+      st = attention(c, l, B, n, pos0, causal);
+      if (st != DG_OK) return st;
+    }
     int s2 = 1;
     st = gemm_dense(c, lm.wo, c->m_o64, c->d, T, c->HD, &s2);
     if (st != DG_OK) return st;
@@ -545,6 +673,7 @@ SampleArgs merge_args(const dg_ctx* c, int T, bool stats_only) {
   a.T = T;
   a.C = c->cfg.canvas;
   a.P = c->P;
+  a.P_seq = c->ragged ? c->rg_lens : nullptr;
   a.vocab = c->V;
   a.stats_only = stats_only ? 1 : 0;
   a.dbg_argmax = c->dbg_argmax;
@@ -647,6 +776,7 @@ EntropyArgs entropy_args(const dg_ctx* c, const EntropyCall& e) {
   memset(&a, 0, sizeof(a));
   a.C = c->cfg.canvas;
   a.P = c->P;
+  a.P_seq = c->ragged ? c->rg_lens : nullptr;
   a.step = e.step;
   a.vocab = c->V;
   a.seed_lo = static_cast<uint32_t>(e.seed & 0xFFFFFFFFull);
@@ -678,8 +808,6 @@ dg_status lm_head_and_entropy_sample(dg_ctx* c, int B, const EntropyCall& e) {
   return DG_OK;
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
-
 template <typename T>
 T* carve(char*& cur, size_t count) {
   T* p = reinterpret_cast<T*>(cur);
@@ -693,7 +821,6 @@ constexpr int kMaxRows = 32768;
 static_assert(PERM_MAXE == MOE_MAX_EXPERTS, "routing and expert GEMM agree on the expert limit");
 
 // every kernel's dynamic shared memory fits the 227 KB a CTA may opt into
-constexpr int kMaxSmemPerCta = 232448;
 static_assert(gemm_smem_bytes<GEMM_DENSE>() <= kMaxSmemPerCta, "dense GEMM shared memory");
 static_assert(gemm_smem_bytes<GEMM_MOE>() <= kMaxSmemPerCta, "expert GEMM shared memory");
 static_assert(gemm_smem_bytes<GEMM_LMHEAD>() <= kMaxSmemPerCta, "LM-head GEMM shared memory");
@@ -787,6 +914,7 @@ dg_status capture_step(dg_ctx* c, int mode) {
   c->launches = l0;
   sg.B = c->B;
   sg.P = c->P;
+  sg.ragged = c->ragged;
   sg.sc = c->sc_enabled;
   return DG_OK;
 }
@@ -807,6 +935,10 @@ dg_status rebind_embed(dg_ctx* c, StepGraph& sg, const int32_t* canvas_in, int32
   return DG_OK;
 }
 
+bool step_graph_fits(const dg_ctx* c, const StepGraph& sg) {
+  return sg.exec && sg.B == c->B && sg.ragged == c->ragged && (c->ragged || sg.P == c->P) && sg.sc == c->sc_enabled;
+}
+
 dg_status launch_graph(dg_ctx* c, StepGraph& sg) {
   DG_CUDA(c, cudaGraphLaunch(sg.exec, c->stream));
   c->launches += sg.launches;
@@ -818,7 +950,7 @@ dg_status launch_graph(dg_ctx* c, StepGraph& sg) {
 dg_status step_via_graph(dg_ctx* c, const int32_t* canvas_in, int32_t step, uint64_t seed, float tau,
                          int32_t* canvas_out, float* conf, int32_t* settled) {
   StepGraph& sg = c->graphs[SAMPLER_TAU];
-  if (!sg.exec || sg.B != c->B || sg.P != c->P || sg.sc != c->sc_enabled) {
+  if (!step_graph_fits(c, sg)) {
     dg_status st = capture_step(c, SAMPLER_TAU);
     if (st != DG_OK) return st;
   }
@@ -845,7 +977,7 @@ dg_status step_via_graph(dg_ctx* c, const int32_t* canvas_in, int32_t step, uint
 // head (temperature) and the entropy sampler (its arguments)
 dg_status entropy_step_via_graph(dg_ctx* c, const int32_t* canvas_in, const EntropyCall& e) {
   StepGraph& sg = c->graphs[SAMPLER_ENTROPY];
-  if (!sg.exec || sg.B != c->B || sg.P != c->P || sg.sc != c->sc_enabled) {
+  if (!step_graph_fits(c, sg)) {
     dg_status st = capture_step(c, SAMPLER_ENTROPY);
     if (st != DG_OK) return st;
   }
@@ -878,7 +1010,9 @@ void free_all(dg_ctx* c) {
   if (c->cap_idx) cudaFree(c->cap_idx);
   if (c->cap_u) cudaFree(c->cap_u);
   if (c->sc_ws) cudaFree(c->sc_ws);
+  if (c->rg_ws) cudaFree(c->rg_ws);
   c->sc_ws = nullptr;
+  c->rg_ws = nullptr;
   c->ws = nullptr;
   c->kcache = c->vcache = nullptr;
   c->cap_h = nullptr;
@@ -1187,6 +1321,8 @@ dg_status dg_prefill(dg_ctx* c, const int32_t* tokens, int32_t B, int32_t P) {
     return fail(c, DG_ERR_CAPACITY, "prefill: batch %d / length %d beyond capacity", B, P);
   c->B = B;
   c->P = 0;
+  c->ragged = false;
+  c->lens.assign(B, P);
   c->prefilled = false;
   c->sc_valid = false;  // a new canvas starts without a self-conditioning signal
   const int chunk = std::max(1, c->R / B);
@@ -1196,6 +1332,85 @@ dg_status dg_prefill(dg_ctx* c, const int32_t* tokens, int32_t B, int32_t P) {
     if (st != DG_OK) return st;
   }
   c->P = P;
+  c->prefilled = true;
+  return DG_OK;
+}
+
+dg_status dg_prefill_ragged(dg_ctx* c, const int32_t* tokens, int32_t B, const int32_t* lens) {
+  if (!c) return DG_ERR_INVALID_ARG;
+  if (!tokens || !lens || B <= 0) return fail(c, DG_ERR_INVALID_ARG, "prefill_ragged: bad arguments");
+  if (B > c->cfg.max_batch) return fail(c, DG_ERR_CAPACITY, "prefill_ragged: batch %d beyond capacity", B);
+  int64_t total = 0;
+  int32_t longest = 0;
+  for (int b = 0; b < B; ++b) {
+    if (lens[b] <= 0) return fail(c, DG_ERR_INVALID_ARG, "prefill_ragged: sequence %d has no token", b);
+    if (lens[b] > c->cfg.max_seq - c->cfg.canvas)
+      return fail(c, DG_ERR_CAPACITY, "prefill_ragged: length %d of sequence %d beyond capacity", lens[b], b);
+    total += lens[b];
+    longest = std::max(longest, lens[b]);
+  }
+  const int width = (c->cfg.max_seq + kRaggedPage - 1) / kRaggedPage;
+  const int pages = static_cast<int>(static_cast<int64_t>(c->cfg.max_batch) * c->cfg.max_seq / kRaggedPage);
+  const std::vector<int32_t> want(lens, lens + B);
+  if (ragged_pages(want, c->cfg.canvas) > pages)
+    return fail(c, DG_ERR_CAPACITY, "prefill_ragged: the batch needs more than the cache's %d pages of %d positions",
+                pages, kRaggedPage);
+  if (!c->rg_ws) {
+    if (!paged_device_sms()) return fail(c, DG_ERR_CUDA, "prefill_ragged: kernel set-up");
+    const size_t mb = c->cfg.max_batch;
+    const int64_t attn = paged_workspace(false, c->D, c->sms);
+    size_t bytes = 0;
+    for (size_t n : {mb, mb, mb * width, static_cast<size_t>(pages), size_t(8), mb + 1, mb, static_cast<size_t>(c->R),
+                     static_cast<size_t>(c->R)})
+      bytes += (n * 4 + 255) / 256 * 256;
+    if (cudaMalloc(&c->rg_ws, bytes + attn) != cudaSuccess) {
+      c->rg_ws = nullptr;
+      cudaGetLastError();
+      return fail(c, DG_ERR_OOM, "prefill_ragged: %zu bytes", bytes + static_cast<size_t>(attn));
+    }
+    char* at = static_cast<char*>(c->rg_ws);
+    c->rg_lens = carve<int32_t>(at, mb);
+    c->rg_new = carve<int32_t>(at, mb);
+    c->rg_table = carve<int32_t>(at, mb * width);
+    c->rg_ring = carve<int32_t>(at, pages);
+    c->rg_state = carve<int32_t>(at, 8);
+    c->rg_cu = carve<int32_t>(at, mb + 1);
+    c->rg_kv = carve<int32_t>(at, mb);
+    c->rg_pos = carve<int32_t>(at, c->R);
+    c->rg_slots = carve<int32_t>(at, c->R);
+    c->rg_attn = at;
+    c->rg_pages = pages;
+    c->rg_width = width;
+  }
+  c->B = B;
+  c->P = 0;
+  c->ragged = true;
+  c->prefilled = false;
+  c->sc_valid = false;  // a new canvas starts without a self-conditioning signal
+  c->lens.assign(B, 0);
+  c->rg_cur = 0;
+  std::vector<int32_t> ring(pages);
+  for (int i = 0; i < pages; ++i) ring[i] = i;
+  const int32_t state[4] = {0, pages, 0, 0};
+  DG_CUDA(c, cudaMemsetAsync(c->rg_lens, 0, B * 4, c->stream));
+  DG_CUDA(c, cudaMemcpyAsync(c->rg_ring, ring.data(), ring.size() * 4, cudaMemcpyHostToDevice, c->stream));
+  DG_CUDA(c, cudaMemcpyAsync(c->rg_state, state, sizeof(state), cudaMemcpyHostToDevice, c->stream));
+  // stretches of up to R packed tokens: the end of one sequence, some whole ones, the start of another
+  for (int64_t x = 0; x < total; x += c->R) {
+    const int64_t end = std::min<int64_t>(total, x + c->R);
+    std::vector<int32_t> rows(B);
+    int64_t off = 0;
+    for (int b = 0; b < B; off += lens[b++])
+      rows[b] = static_cast<int32_t>(std::max<int64_t>(0, std::min<int64_t>(end, off + lens[b]) - std::max(x, off)));
+    dg_status st = ragged_plan(c, rows);
+    const int n = static_cast<int>(end - x);
+    if (st == DG_OK) st = forward(c, tokens + x, n, 0, 1, n, 0, true, nullptr);
+    if (st == DG_OK) st = ragged_adopt(c, rows);
+    if (st != DG_OK) return st;
+  }
+  c->P = longest;
+  const dg_status st = ragged_plan(c, std::vector<int32_t>(B, c->cfg.canvas));  // the canvases' rows
+  if (st != DG_OK) return st;
   c->prefilled = true;
   return DG_OK;
 }
@@ -1262,8 +1477,18 @@ dg_status dg_commit_block(dg_ctx* c, const int32_t* block) {
   if (!c->prefilled) return fail(c, DG_ERR_STATE, "commit before prefill");
   if (c->P + 2 * c->cfg.canvas > c->cfg.max_seq)
     return fail(c, DG_ERR_CAPACITY, "commit: no room for another block");
+  if (c->ragged && ragged_pages(c->lens, 2 * c->cfg.canvas) > c->rg_pages)
+    return fail(c, DG_ERR_CAPACITY, "commit: no pages for another block");
   dg_status st = forward(c, block, c->cfg.canvas, 0, c->B, c->cfg.canvas, c->P, true, nullptr);
   if (st != DG_OK) return st;
+  if (c->ragged) {
+    const std::vector<int32_t> rows(c->B, c->cfg.canvas);
+    st = ragged_adopt(c, rows);
+    if (st == DG_OK) st = ragged_plan(c, rows);  // the next canvases' rows
+    if (st != DG_OK) return st;
+  } else {
+    for (int32_t& x : c->lens) x += c->cfg.canvas;
+  }
   c->P += c->cfg.canvas;
   c->sc_valid = false;  // the next block starts without a self-conditioning signal
   return DG_OK;
@@ -1283,6 +1508,12 @@ dg_status dg_sync(dg_ctx* c) {
 }
 
 int32_t dg_cached_len(const dg_ctx* c) { return c ? c->P : -1; }
+
+dg_status dg_cached_lens(const dg_ctx* c, int32_t* lens) {
+  if (!c || !lens) return DG_ERR_INVALID_ARG;
+  std::copy(c->lens.begin(), c->lens.begin() + (c->prefilled ? c->B : 0), lens);
+  return DG_OK;
+}
 
 const char* dg_last_error(const dg_ctx* c) {
   if (c) return c->last_error.c_str();
@@ -1354,7 +1585,8 @@ dg_status dg_debug_sample(dg_ctx* c, const int32_t* argmax, const float* conf, i
                           uint64_t seed, float tau, int32_t* out) {
   if (!c || !argmax || !conf || !out || B <= 0) return fail(c, DG_ERR_INVALID_ARG, "debug_sample");
   const int T = B * c->cfg.canvas;
-  sample_only_kernel<<<(T + 255) / 256, 256, 0, c->stream>>>(argmax, conf, T, c->cfg.canvas, c->P, step,
+  sample_only_kernel<<<(T + 255) / 256, 256, 0, c->stream>>>(argmax, conf, T, c->cfg.canvas, c->P,
+                                                              c->ragged ? c->rg_lens : nullptr, step,
                                                               static_cast<uint32_t>(seed & 0xFFFFFFFFull),
                                                               static_cast<uint32_t>(seed >> 32), tau, c->V, out);
   DG_LAUNCHED(c);
@@ -1370,6 +1602,7 @@ dg_status dg_debug_entropy_sample(dg_ctx* c, const int32_t* argmax, const float*
   memset(&a, 0, sizeof(a));
   a.C = c->cfg.canvas;
   a.P = c->P;
+  a.P_seq = c->ragged ? c->rg_lens : nullptr;
   a.step = step;
   a.vocab = c->V;
   a.seed_lo = static_cast<uint32_t>(seed & 0xFFFFFFFFull);
@@ -1537,7 +1770,6 @@ constexpr size_t kLmStaticPartials = 524288;  // float4 entries = 8 MiB: n_rows 
 static __device__ __align__(256) float4 g_lm_static_partials[kLmStaticPartials];
 static __device__ __align__(256) int g_lm_static_err[4];
 
-constexpr int kMaxDevices = 64;
 struct StaticSetup {
   bool done = false;
   float4* partials = nullptr;  // device address of g_lm_static_partials on this device
@@ -1626,5 +1858,3 @@ extern "C" dg_status dg_lmhead_argmax_static(const void* z, int32_t n_rows, int3
     return DG_ERR_CUDA;
   return DG_OK;
 }
-
-#include "paged_api.cuh"

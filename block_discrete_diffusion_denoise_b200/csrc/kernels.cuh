@@ -541,6 +541,7 @@ __device__ __forceinline__ float merged_entropy(const Top2& a) {
 
 struct SampleArgs {
   int n_vtiles, T, C, P, step, vocab;
+  const int32_t* P_seq;    // cached length of each sequence (ragged batch) or NULL: P for all
   uint32_t seed_lo, seed_hi;
   float tau;
   int stats_only;          // 1: write the statistics only (the entropy sampler decides)
@@ -575,7 +576,8 @@ __global__ void lmhead_merge_sample_kernel(const float4* __restrict__ part, Samp
     const float margin = (1.f - exp2f(acc.m2 - acc.m1)) / acc.s;
     const int b = t / a.C, i = t % a.C;
     if (!a.stats_only) {
-      const int out = sample_decision(acc.idx, conf, a.tau, a.P + i, a.step, b, a.seed_lo, a.seed_hi, a.vocab);
+      const int P = a.P_seq ? a.P_seq[b] : a.P;
+      const int out = sample_decision(acc.idx, conf, a.tau, P + i, a.step, b, a.seed_lo, a.seed_hi, a.vocab);
       a.canvas_out[t] = out;
       if (a.conf_out) a.conf_out[t] = conf;
       if (a.settled && !(conf >= a.tau)) a.settled[b] = 0;
@@ -603,6 +605,7 @@ __global__ void lmhead_merge_sample_kernel(const float4* __restrict__ part, Samp
 // float32 entropies.  argmax_out (may equal prev_argmax) receives the argmax.
 struct EntropyArgs {
   int C, P, step, vocab;
+  const int32_t* P_seq;       // cached length of each sequence (ragged batch) or NULL: P for all
   uint32_t seed_lo, seed_hi;
   float gamma, stop_entropy;
   const int32_t* argmax;      // [B*C] (merged statistics)
@@ -655,7 +658,8 @@ __global__ void __launch_bounds__(256) entropy_sample_kernel(EntropyArgs a) {
   for (int j = 0; j < a.C; ++j) rank += (se[j] < e || (se[j] == e && j < i)) ? 1 : 0;
   int out = am;
   if (!s_stop && rank >= s_count) {
-    const uint4 r = philox4x32_10(make_uint4(static_cast<uint32_t>(a.P + i), static_cast<uint32_t>(a.step),
+    const int P = a.P_seq ? a.P_seq[b] : a.P;
+    const uint4 r = philox4x32_10(make_uint4(static_cast<uint32_t>(P + i), static_cast<uint32_t>(a.step),
                                              static_cast<uint32_t>(b), 0u),
                                   make_uint2(a.seed_lo, a.seed_hi));
     out = uniform_token(r.x, a.vocab);
@@ -668,12 +672,12 @@ __global__ void __launch_bounds__(256) entropy_sample_kernel(EntropyArgs a) {
 
 // sampler alone (test hook): given argmax / conf
 __global__ void sample_only_kernel(const int32_t* __restrict__ argmax, const float* __restrict__ conf, int T,
-                                   int C, int P, int step, uint32_t seed_lo, uint32_t seed_hi, float tau,
+                                   int C, int P, const int32_t* __restrict__ P_seq, int step, uint32_t seed_lo, uint32_t seed_hi, float tau,
                                    int vocab, int32_t* __restrict__ out) {
   DG_TIMELINE_SCOPE(TLK_SAMPLE_ONLY);
   const int t = blockIdx.x * blockDim.x + threadIdx.x;
   if (t >= T) return;
-  out[t] = sample_decision(argmax[t], conf[t], tau, P + t % C, step, t / C, seed_lo, seed_hi, vocab);
+  out[t] = sample_decision(argmax[t], conf[t], tau, (P_seq ? P_seq[t / C] : P) + t % C, step, t / C, seed_lo, seed_hi, vocab);
 }
 
 // waits on a barrier that is never signalled; the bounded wait must give up

@@ -179,6 +179,8 @@ constexpr int APPEND_HEADS = 4;
 struct PagedAppendParams {
   const uint16_t* qkv;         // [rows][(Hq + 2 Hkv) D], row stride qkv_stride
   int64_t qkv_stride;
+  const float* part;           // or the split-K sums of the projection [splits][rows][(Hq + 2 Hkv) D], added in order
+  int splits;
   const int32_t* positions;
   const int32_t* slots;
   const float4* rope;          // [n_positions][D/2] (cos, sin)
@@ -203,7 +205,38 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
-template <int D>
+// eight columns of a row as fp32: split sums added in order, or bf16 values
+template <bool SPLITS>
+struct AppendIn {
+  float f[8];
+  __device__ __forceinline__ void load(const PagedAppendParams& p, int64_t row, int64_t width, int64_t col) {
+    const float* src = p.part + row * width + col;
+    float4 a = *reinterpret_cast<const float4*>(src), b = *reinterpret_cast<const float4*>(src + 4);
+    for (int s = 1; s < p.splits; ++s) {
+      src += p.rows * width;
+      const float4 x = *reinterpret_cast<const float4*>(src), y = *reinterpret_cast<const float4*>(src + 4);
+      a = make_float4(a.x + x.x, a.y + x.y, a.z + x.z, a.w + x.w);
+      b = make_float4(b.x + y.x, b.y + y.y, b.z + y.z, b.w + y.w);
+    }
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w, f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = f[e];
+  }
+  __device__ __forceinline__ uint4 bits() const { return pack8(f); }
+};
+template <>
+struct AppendIn<false> {
+  uint4 u;
+  __device__ __forceinline__ void load(const PagedAppendParams& p, int64_t row, int64_t, int64_t col) {
+    u = *reinterpret_cast<const uint4*>(p.qkv + row * p.qkv_stride + col);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack8(u, v); }
+  __device__ __forceinline__ uint4 bits() const { return u; }
+};
+
+template <int D, bool SPLITS>
 __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   DG_TIMELINE_SCOPE(TLK_OTHER);
   constexpr int HALF = D / 2, C = HALF / 8;  // chunks of eight pairs in a head
@@ -219,13 +252,12 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
   const int pos = p.positions[row], slot = p.slots[row];
   const bool known = pos >= 0 && pos < p.n_positions;
   const bool kept = known && slot >= 0 && slot < p.n_slots;
-  const uint16_t* src = p.qkv + row * p.qkv_stride + c * 8;
-  uint4 lo[APPEND_HEADS], hi[APPEND_HEADS];
+  AppendIn<SPLITS> lo[APPEND_HEADS], hi[APPEND_HEADS];
 #pragma unroll
   for (int i = 0; i < APPEND_HEADS; ++i)
     if (h0 + i < heads) {
-      lo[i] = *reinterpret_cast<const uint4*>(src + (h0 + i) * D);
-      hi[i] = *reinterpret_cast<const uint4*>(src + (h0 + i) * D + HALF);
+      lo[i].load(p, row, heads * D, (h0 + i) * D + c * 8);
+      hi[i].load(p, row, heads * D, (h0 + i) * D + c * 8 + HALF);
     }
   float cs[8], sn[8];
 #pragma unroll
@@ -242,17 +274,21 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
   for (int i = 0; i < APPEND_HEADS; ++i) {
     const int h = h0 + i;
     if (h >= heads) break;
+    uint4 out_lo, out_hi;
     if (h < p.Hq + p.Hkv) {
       float a[8], b[8], x[8], y[8];
-      unpack8(lo[i], a);
-      unpack8(hi[i], b);
+      lo[i].get(a);
+      hi[i].get(b);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         x[e] = a[e] * cs[e] - b[e] * sn[e];
         y[e] = b[e] * cs[e] + a[e] * sn[e];
       }
-      lo[i] = pack8(x);
-      hi[i] = pack8(y);
+      out_lo = pack8(x);
+      out_hi = pack8(y);
+    } else {
+      out_lo = lo[i].bits();
+      out_hi = hi[i].bits();
     }
     uint16_t* dst;
     if (h < p.Hq) {
@@ -263,8 +299,8 @@ __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __gr
       dst = (h < p.Hq + p.Hkv ? p.k : p.v) +
             (((static_cast<int64_t>(page) * p.Hkv + g) << p.page_shift) + off) * D;
     }
-    *reinterpret_cast<uint4*>(dst + c * 8) = lo[i];
-    *reinterpret_cast<uint4*>(dst + c * 8 + HALF) = hi[i];
+    *reinterpret_cast<uint4*>(dst + c * 8) = out_lo;
+    *reinterpret_cast<uint4*>(dst + c * 8 + HALF) = out_hi;
   }
 }
 

@@ -1,6 +1,7 @@
 // C ABI of the paged KV cache (include/dg.h, dg_paged_*): argument checks on
 // the host, launch shapes, and the choice of the attention kernel.  Included
-// by engine.cu, whose tensor-map helpers it uses.
+// by engine.cu, whose tensor-map helpers it uses and whose ragged batches make
+// the same launches.
 #pragma once
 
 #include <atomic>
@@ -45,6 +46,16 @@ dg_status paged_launch(void (*kernel)(P), dim3 grid, int threads, size_t smem, v
   lc.attrs = &attr;
   lc.numAttrs = 1;
   return cudaLaunchKernelEx(&lc, kernel, p) == cudaSuccess ? DG_OK : DG_ERR_CUDA;
+}
+
+template <bool SPLITS>
+dg_status launch_append(const PagedAppendParams& p, int head_dim, void* stream) {
+  const int groups = (p.Hq + 2 * p.Hkv + APPEND_HEADS - 1) / APPEND_HEADS;
+  const int64_t grid = (static_cast<int64_t>(p.rows) * groups * (head_dim / 16) + APPEND_THREADS - 1) / APPEND_THREADS;
+  if (grid > INT32_MAX) return DG_ERR_CAPACITY;
+  auto* kern = head_dim == 64 ? paged_append_kernel<64, SPLITS>
+               : head_dim == 128 ? paged_append_kernel<128, SPLITS> : paged_append_kernel<176, SPLITS>;
+  return paged_launch(kern, dim3(static_cast<unsigned>(grid)), APPEND_THREADS, 0, stream, p);
 }
 
 // What the attention calls need of a device: its SM count, and the kernels'
@@ -112,14 +123,13 @@ dg_status check_attention(const dg_paged_attention_args* a) {
 
 // Tiles of 16 packed rows for requests whose rows fit one (they are bound by
 // the stream of pages), of 256 on the tensor cores' accumulators above it.
-bool few_rows(const dg_paged_attention_args* a) {
-  const int rows = a->max_rows > 0 && a->max_rows < a->n_rows ? a->max_rows : a->n_rows;
-  return static_cast<int64_t>(rows) * (a->n_q_heads / a->n_kv_heads) <= TOK_ROWS;
+bool few_rows(int64_t rows, int64_t max_rows, int G) {
+  return (max_rows > 0 && max_rows < rows ? max_rows : rows) * G <= TOK_ROWS;
 }
 
-int64_t paged_workspace(const dg_paged_attention_args* a, int sms) {
-  const int64_t rows = few_rows(a) ? TOK_ROWS : CV_ROWS;
-  return 2 * sms * rows * (a->head_dim * 4 + 8) + sms * static_cast<int64_t>(sizeof(PagedCut));
+int64_t paged_workspace(bool few, int head_dim, int sms) {
+  const int64_t rows = few ? TOK_ROWS : CV_ROWS;
+  return 2 * sms * rows * (head_dim * 4 + 8) + sms * static_cast<int64_t>(sizeof(PagedCut));
 }
 
 // Queries [row][Hq][D] seen as (D, G, Hkv, row): a box of 64 columns x G heads
@@ -155,6 +165,25 @@ template <int D>
 dg_status launch_canvas(const CanvasParams& p, int tiles, int sms, void* stream) {
   const dg_status st = paged_launch(paged_canvas_kernel<D>, dim3(sms), CV_THREADS, CvCfg<D>::SMEM, stream, p);
   return st != DG_OK ? st : launch_merge<CV_ROWS, D>(p.a, tiles, sms, stream);
+}
+
+// Attention with everything of p set but the workspace's parts and the lists:
+// the kernel for tiles of 16 or of 256 rows, then the merge.
+dg_status launch_attention(CanvasParams& cp, bool few, int head_dim, void* workspace, int sms, void* stream) {
+  PagedAttnParams& p = cp.a;
+  const int64_t tile_rows = few ? TOK_ROWS : CV_ROWS, slots = 2 * static_cast<int64_t>(sms) * tile_rows;
+  p.part = static_cast<float*>(workspace);
+  p.part_ml = reinterpret_cast<float2*>(p.part + slots * head_dim);
+  p.cuts = reinterpret_cast<PagedCut*>(p.part_ml + slots);
+  // tiles: ceil(rows_b * G / ROWS) over the requests, per kv head
+  const int64_t tiles64 = (static_cast<int64_t>(p.rows) * (p.Hq / p.Hkv) / tile_rows + p.batch) * p.Hkv;
+  const int tiles = static_cast<int>(std::min<int64_t>(tiles64, sms));
+  p.cuts_by_tile = tiles64 <= sms ? tiles : 0;
+  switch (head_dim) {
+    case 64: return few ? launch_token<64>(p, tiles, sms, stream) : launch_canvas<64>(cp, tiles, sms, stream);
+    case 128: return few ? launch_token<128>(p, tiles, sms, stream) : launch_canvas<128>(cp, tiles, sms, stream);
+    default: return few ? launch_token<176>(p, tiles, sms, stream) : launch_canvas<176>(cp, tiles, sms, stream);
+  }
 }
 
 }  // namespace
@@ -215,7 +244,7 @@ dg_status dg_paged_append(const void* qkv, int64_t qkv_stride, int32_t n_rows, i
   if (qkv_stride < static_cast<int64_t>(heads) * head_dim || qkv_stride % 8) return DG_ERR_INVALID_ARG;
   if (n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;
   if (n_rows == 0) return DG_OK;
-  PagedAppendParams p;
+  PagedAppendParams p{};
   p.qkv = static_cast<const uint16_t*>(qkv);
   p.qkv_stride = qkv_stride;
   p.positions = positions;
@@ -230,12 +259,7 @@ dg_status dg_paged_append(const void* qkv, int64_t qkv_stride, int32_t n_rows, i
   p.Hq = n_q_heads;
   p.Hkv = n_kv_heads;
   p.page_shift = shift;
-  const int64_t items = static_cast<int64_t>(n_rows) * ((heads + APPEND_HEADS - 1) / APPEND_HEADS) * (head_dim / 16);
-  const int64_t grid = (items + APPEND_THREADS - 1) / APPEND_THREADS;
-  if (grid > INT32_MAX) return DG_ERR_CAPACITY;
-  auto* kern = head_dim == 64 ? paged_append_kernel<64>
-               : head_dim == 128 ? paged_append_kernel<128> : paged_append_kernel<176>;
-  return paged_launch(kern, dim3(static_cast<unsigned>(grid)), APPEND_THREADS, 0, cuda_stream, p);
+  return launch_append<false>(p, head_dim, cuda_stream);
 }
 
 dg_status dg_paged_attention_workspace(const dg_paged_attention_args* a, int64_t* bytes) {
@@ -243,7 +267,7 @@ dg_status dg_paged_attention_workspace(const dg_paged_attention_args* a, int64_t
   if (st != DG_OK || !bytes) return bytes ? st : DG_ERR_INVALID_ARG;
   const int sms = paged_device_sms();
   if (!sms) return DG_ERR_CUDA;
-  *bytes = paged_workspace(a, sms);
+  *bytes = paged_workspace(few_rows(a->n_rows, a->max_rows, a->n_q_heads / a->n_kv_heads), a->head_dim, sms);
   return DG_OK;
 }
 
@@ -254,11 +278,11 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   if (!a->workspace || !aligned16(a->workspace)) return DG_ERR_INVALID_ARG;
   const int sms = paged_device_sms();
   if (!sms) return DG_ERR_CUDA;
-  if (a->workspace_bytes < paged_workspace(a, sms)) return DG_ERR_CAPACITY;
+  const bool few = few_rows(a->n_rows, a->max_rows, a->n_q_heads / a->n_kv_heads);
+  if (a->workspace_bytes < paged_workspace(few, a->head_dim, sms)) return DG_ERR_CAPACITY;
   const int shift = page_shift_of(a->page_size);
   CanvasParams cp;
   PagedAttnParams& p = cp.a;
-  const bool few = few_rows(a);
   const uint64_t pool_rows = (static_cast<uint64_t>(a->n_pages) * a->n_kv_heads) << shift;
   const uint32_t box = std::min(a->page_size, PG_BK);
   if (!make_map(&p.k_map, a->k_pages, pool_rows, a->head_dim, box) ||
@@ -272,10 +296,6 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   p.cu_rows = a->cu_rows;
   p.o = static_cast<uint16_t*>(a->out);
   p.lse = a->lse;
-  p.part = static_cast<float*>(a->workspace);
-  const int64_t part_rows = 2 * static_cast<int64_t>(sms) * (few ? TOK_ROWS : CV_ROWS);
-  p.part_ml = reinterpret_cast<float2*>(p.part + part_rows * a->head_dim);
-  p.cuts = reinterpret_cast<PagedCut*>(p.part_ml + part_rows);
   p.rows = a->n_rows;
   p.batch = a->batch;
   p.Hq = a->n_q_heads;
@@ -286,17 +306,7 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   p.causal = a->causal != 0;
   p.scale_log2 = static_cast<float>(1.4426950408889634 * static_cast<double>(a->scale));
   p.err = DevErr{nullptr, 1000000000ull};
-  // tiles: ceil(rows_b * G / ROWS) over the requests, per kv head
-  const int64_t tile_rows = few ? TOK_ROWS : CV_ROWS;
-  const int64_t tiles64 =
-      (static_cast<int64_t>(a->n_rows) * (a->n_q_heads / a->n_kv_heads) / tile_rows + a->batch) * a->n_kv_heads;
-  const int tiles = static_cast<int>(std::min<int64_t>(tiles64, sms));
-  p.cuts_by_tile = tiles64 <= sms ? tiles : 0;
-  switch (a->head_dim) {
-    case 64: return few ? launch_token<64>(p, tiles, sms, cuda_stream) : launch_canvas<64>(cp, tiles, sms, cuda_stream);
-    case 128: return few ? launch_token<128>(p, tiles, sms, cuda_stream) : launch_canvas<128>(cp, tiles, sms, cuda_stream);
-    default: return few ? launch_token<176>(p, tiles, sms, cuda_stream) : launch_canvas<176>(cp, tiles, sms, cuda_stream);
-  }
+  return launch_attention(cp, few, a->head_dim, a->workspace, sms, cuda_stream);
 }
 
 }  // extern "C"

@@ -142,6 +142,19 @@ dg_status dg_destroy(dg_ctx* ctx);
  * Needs batch <= max_batch and prefix_len + canvas <= max_seq. */
 dg_status dg_prefill(dg_ctx* ctx, const int32_t* tokens_dev, int32_t batch, int32_t prefix_len);
 
+/* The same for sequences of different lengths (a ragged batch): tokens_dev
+ * holds the prompts one behind another, sequence b's being lens_host[b] int32
+ * tokens (a HOST array of batch lengths, each > 0, read during the call).
+ * The context's cache then serves as a pool of pages of 64 positions shared by
+ * the sequences: each needs lens + canvas <= max_seq, and all of them together
+ * ceil((lens + canvas) / 64) pages of the floor(max_batch * max_seq / 64) that
+ * there are (DG_ERR_CAPACITY otherwise; with max_seq a multiple of 64 no
+ * sequence is ever short of pages).  The denoising steps and
+ * dg_commit_block then work as after dg_prefill, each sequence at its own
+ * positions [P_b, P_b + canvas).  The first call allocates the plan's and the
+ * attention's buffers (about 55 MB at head_dim 176). */
+dg_status dg_prefill_ragged(dg_ctx* ctx, const int32_t* tokens_dev, int32_t batch, const int32_t* lens_host);
+
 /* One denoising step over the canvas (codemajin.net sections 3.1-3.3):
  * canvas_in_dev [batch, canvas] int32 tokens at positions [P, P+canvas) are
  * run through every layer with bidirectional attention over cache[0,P) plus
@@ -154,7 +167,7 @@ dg_status dg_prefill(dg_ctx* ctx, const int32_t* tokens_dev, int32_t batch, int3
  *   all_settled_dev [batch] int32 or NULL: 1 where every conf >= tau, else 0.
  * The committed cache is not modified.  canvas_out_dev may equal
  * canvas_in_dev; other outputs must not alias inputs.  batch is the batch of
- * the last dg_prefill. */
+ * the last dg_prefill or dg_prefill_ragged. */
 dg_status dg_denoise_step(dg_ctx* ctx, const int32_t* canvas_in_dev, int32_t step, uint64_t seed,
                           float tau, int32_t* canvas_out_dev, float* conf_dev,
                           int32_t* all_settled_dev);
@@ -221,8 +234,13 @@ dg_status dg_commit_block(dg_ctx* ctx, const int32_t* block_dev);
 /* Wait for all work of ctx and report device-side errors. */
 dg_status dg_sync(dg_ctx* ctx);
 
-/* Committed cache length P (tokens per sequence). */
+/* Committed cache length P (tokens per sequence; in a ragged batch the
+ * longest). */
 int32_t dg_cached_len(const dg_ctx* ctx);
+
+/* Committed cache length of every sequence: lens_host [batch of the last
+ * prefill] int32 (nothing is written before a prefill). */
+dg_status dg_cached_lens(const dg_ctx* ctx, int32_t* lens_host);
 
 /* Message for the last failed call on ctx (never NULL).  With ctx == NULL:
  * the calling thread's last dg_create failure (a failed create returns no
