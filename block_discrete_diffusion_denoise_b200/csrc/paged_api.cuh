@@ -172,6 +172,8 @@ dg_status launch_canvas(const CanvasParams& p, int tiles, int sms, void* stream)
 dg_status launch_attention(CanvasParams& cp, bool few, int head_dim, void* workspace, int sms, void* stream) {
   PagedAttnParams& p = cp.a;
   const int64_t tile_rows = few ? TOK_ROWS : CV_ROWS, slots = 2 * static_cast<int64_t>(sms) * tile_rows;
+  p.g_shift = 0;
+  while (p.Hkv << p.g_shift < p.Hq) ++p.g_shift;
   p.part = static_cast<float*>(workspace);
   p.part_ml = reinterpret_cast<float2*>(p.part + slots * head_dim);
   p.cuts = reinterpret_cast<PagedCut*>(p.part_ml + slots);

@@ -43,6 +43,7 @@ struct PagedAttnParams {
   float2* part_ml;             // [CTA][2][tile rows] their (max in log2 units, sum)
   PagedCut* cuts;              // [CTA], or with cuts_by_tile [tile]
   int rows, batch, Hq, Hkv, n_pages, page_shift, width, causal;
+  int g_shift;                 // log2 of the group size Hq / Hkv, a divisor of 128
   int cuts_by_tile;            // entries of `cuts` by tile where the call has at most as many tiles as CTAs, else 0
   float scale_log2;            // log2(e) * scale
   DevErr err;
@@ -58,7 +59,7 @@ __device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams& p, 
   r.t0 = min(max(p.cu_rows[b], 0), p.rows);
   r.n = max(min(p.cu_rows[b + 1], p.rows) - r.t0, 0);
   r.kv = min(max(p.kv_lens[b], 0), p.width << p.page_shift);
-  r.tiles = (r.n * (p.Hq / p.Hkv) + ROWS - 1) / ROWS;
+  r.tiles = ((r.n << p.g_shift) + ROWS - 1) / ROWS;
   return r;
 }
 
@@ -67,7 +68,7 @@ template <int ROWS>
 __device__ __forceinline__ int paged_blocks(const PagedAttnParams& p, const PagedRequest& r, int t) {
   int keys = r.kv;
   if (p.causal && t + 1 < r.tiles)
-    keys = min(keys, r.kv - r.n + ((t + 1) * ROWS - 1) / (p.Hq / p.Hkv) + 1);
+    keys = min(keys, r.kv - r.n + (((t + 1) * ROWS - 1) >> p.g_shift) + 1);
   return keys > 0 ? (keys - 1) / PG_BK + 1 : 1;   // a tile without keys still writes its rows
 }
 
@@ -114,13 +115,14 @@ __device__ __forceinline__ int paged_holder(const PagedRange& g, int64_t u) {
 // One pass over the batch by the whole CTA: each thread sums the units of a
 // run of requests, a scan gives their places on the line, and the thread that
 // finds the stretch's start on its run tells the others.
-template <int ROWS>
+template <int ROWS, int THREADS>
 __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int cta, int ctas) {
-  __shared__ long long warp_sum[16];
-  __shared__ int warp_tiles[16];
+  constexpr int WARPS = THREADS / 32;
+  __shared__ long long warp_sum[WARPS];
+  __shared__ int warp_tiles[WARPS];
   __shared__ PagedRange found;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-  const int per = (p.batch + blockDim.x - 1) / blockDim.x;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int per = (p.batch + THREADS - 1) / THREADS;
   const int b0 = min(static_cast<int>(threadIdx.x) * per, p.batch), b1 = min(b0 + per, p.batch);
   long long sum = 0;
   int tiles = 0;
@@ -150,7 +152,8 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int 
   __syncthreads();
   long long total = 0, before = 0;
   int tiles_all = 0, tiles_before = 0;
-  for (int w = 0; w < warps; ++w) {
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
     if (w == warp) {
       before = total;
       tiles_before = tiles_all;
@@ -257,7 +260,7 @@ __device__ __forceinline__ void paged_list(const PagedAttnParams& p, const Paged
   cut.tiles = g.tiles;
   if (w.kb0 > 0) return;
   if (w.kb1 < w.nb) {
-    cut.rows = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
+    cut.rows = min((w.r.n << p.g_shift) - w.tile * ROWS, ROWS);
     cut.t0 = w.r.t0;
     cut.row0 = w.tile * ROWS;
     cut.h = w.h;
@@ -356,8 +359,8 @@ struct TokDesc {
 
 // (row, column) of a tile's live rows -> the output row
 __device__ __forceinline__ int64_t paged_out_row(const PagedAttnParams& p, int t0, int packed, int h) {
-  const int G = p.Hq / p.Hkv;
-  return static_cast<int64_t>(t0 + packed / G) * p.Hq + h * G + packed % G;
+  const int in_group = packed & ((1 << p.g_shift) - 1);
+  return static_cast<int64_t>(t0 + (packed >> p.g_shift)) * p.Hq + (h << p.g_shift) + in_group;
 }
 
 // NaN in every row a stretch should have written (a wait ran out)
@@ -368,7 +371,7 @@ __device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
   cut.tiles = g.tiles;
   for (PagedWalk<ROWS> w(g); w.more(); w.next(p), ++seg) {
     paged_list<ROWS>(p, g, w, seg, cut);   // every thread writes the same
-    const int live = min(w.r.n * (p.Hq / p.Hkv) - w.tile * ROWS, ROWS);
+    const int live = min((w.r.n << p.g_shift) - w.tile * ROWS, ROWS);
     for (int i = threadIdx.x; i < live * D; i += blockDim.x) {
       const int64_t out = paged_out_row(p, w.r.t0, w.tile * ROWS + i / D, w.h);
       if (w.whole()) {
@@ -418,16 +421,15 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     fence_mbar_init();
   }
   pdl_wait();
-  const PagedRange g = paged_range<TOK_ROWS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
-  const int G = p.Hq / p.Hkv;
+  const PagedRange g = paged_range<TOK_ROWS, TOK_THREADS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
   bool ok = true;
 
   if (warp == 0) {
     // ------------------------------- producer -------------------------------
     const int box = min(1 << p.page_shift, PG_BK);              // keys per TMA box
-    const int pieces = PG_BK / box;                             // pages (or part of one) per block
+    const int piece_shift = max(6 - p.page_shift, 0), pieces = 1 << piece_shift;  // pages (or part of one) per block
     const int rows_per_page = p.Hkv << p.page_shift;
-    const int my_piece = lane % pieces, my_col = lane / pieces; // box of this lane: K columns, then V columns
+    const int my_piece = lane & (pieces - 1), my_col = lane >> piece_shift;  // box of this lane: K columns, then V
     const bool mine = my_col < 2 * C::DK;
     const bool is_v = my_col >= C::DK;
     const int db = is_v ? my_col - C::DK : my_col;
@@ -438,7 +440,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     for (PagedWalk<TOK_ROWS> w(g); ok && w.more(); w.next(p), ++seg) {
       if (lane == 0) paged_list<TOK_ROWS>(p, g, w, seg, cut);
       const int32_t* tab = p.table + w.b * p.table_stride;
-      const int live = min(w.r.n * G - w.tile * TOK_ROWS, TOK_ROWS);
+      const int live = min((w.r.n << p.g_shift) - w.tile * TOK_ROWS, TOK_ROWS);
       int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         const int s = it % C::STAGES;
@@ -486,7 +488,9 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
         if (kb == w.kb0 && lane < live) {
           const int r = w.tile * TOK_ROWS + lane;
           bulk_load(s_q + (seg % C::Q_BUFS) * C::Q_BYTES + lane * D * 2,
-                    p.q + (w.r.t0 + r / G) * p.q_stride + (w.h * G + r % G) * D, D * 2, &full[s]);
+                    p.q + (w.r.t0 + (r >> p.g_shift)) * p.q_stride +
+                        ((w.h << p.g_shift) + (r & ((1 << p.g_shift) - 1))) * D,
+                    D * 2, &full[s]);
         }
         issued |= 1u << s;
         par = (par & ~(1u << s)) | (((it / C::STAGES) & 1) << s);
@@ -531,7 +535,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
         for (int x = 0; x < 2; ++x) {
           m[x] = -INFINITY;
           l[x] = 0.f;
-          lim[x] = p.causal ? min(d.kv, d.kv - d.n + (d.row0 + gr + 8 * x) / G + 1) : d.kv;
+          lim[x] = p.causal ? min(d.kv, d.kv - d.n + ((d.row0 + gr + 8 * x) >> p.g_shift) + 1) : d.kv;
         }
       }
       // S = Q K^T for this warp's 16 keys: two 16 x 8 tiles
@@ -607,7 +611,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       if (!(d.flags & TOK_LAST)) continue;
 
       // -------- the tile's end: the four warps' rows joined in order --------
-      const int live = min(d.n * G - d.row0, TOK_ROWS);
+      const int live = min((d.n << p.g_shift) - d.row0, TOK_ROWS);
       if (seg > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(o_free, (seg - 1) & 1, p.err) && !*abort_flag);
         if (!ok) break;

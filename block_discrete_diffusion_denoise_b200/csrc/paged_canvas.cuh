@@ -190,10 +190,9 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   }
   tc_fence_before();
   pdl_wait();
-  const PagedRange g = paged_range<CV_ROWS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
+  const PagedRange g = paged_range<CV_ROWS, CV_THREADS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  const int G = p.Hq / p.Hkv;
   bool ok = true;
 
   if (warp < 2) {
@@ -204,9 +203,9 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     uint64_t* empty = is_k ? k_empty : v_empty;
     uint8_t* ring = smem + (is_k ? C::K_OFF : C::V_OFF);
     const int box = min(1 << p.page_shift, PG_BK);              // keys per TMA box
-    const int pieces = PG_BK / box;                             // pages (or part of one) per block
+    const int piece_shift = max(6 - p.page_shift, 0), pieces = 1 << piece_shift;  // pages (or part of one) per block
     const int rows_per_page = p.Hkv << p.page_shift;
-    const int my_piece = lane % pieces, db = lane / pieces;     // box of this lane
+    const int my_piece = lane & (pieces - 1), db = lane >> piece_shift;           // box of this lane
     const uint64_t pol = policy_evict_last();                   // the request's other row tiles read the block again
     int it = 0, seg = 0;
     uint32_t issued = 0, par = 0;
@@ -276,10 +275,10 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       __syncwarp();
       if (lane < C::DK)
         tma_load_4d(smem + q * C::Q_BYTES + lane * CV_TILE * 128, &cp.q_map, &q_full[q], lane * 64, 0, w.h,
-                    w.r.t0 + (w.tile * CV_ROWS + q * CV_TILE) / G, policy_evict_last());
+                    w.r.t0 + ((w.tile * CV_ROWS + q * CV_TILE) >> p.g_shift), policy_evict_last());
       ++loads;
     };
-    auto has_rows = [&](const PagedWalk<CV_ROWS>& w) { return w.r.n * G - w.tile * CV_ROWS > q * CV_TILE; };
+    auto has_rows = [&](const PagedWalk<CV_ROWS>& w) { return (w.r.n << p.g_shift) - w.tile * CV_ROWS > q * CV_TILE; };
     bool fetched = false;                    // this tile's queries are on their way
     int j = 0;
     for (PagedWalk<CV_ROWS> w(g); ok && w.more(); w.next(p)) {
@@ -372,15 +371,15 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     int turns = 0;                                   // units so far that both tiles had rows in
     for (PagedWalk<CV_ROWS> w(g); ok && w.more(); w.next(p), ++seg) {
       const int row0 = w.tile * CV_ROWS, units = w.kb1 - w.kb0;
-      if (w.r.n * G - row0 <= wg * CV_TILE) {        // no live row in this tile
+      if ((w.r.n << p.g_shift) - row0 <= wg * CV_TILE) {        // no live row in this tile
         j += units;
         continue;
       }
-      const bool both = w.r.n * G - row0 > CV_TILE;
+      const bool both = (w.r.n << p.g_shift) - row0 > CV_TILE;
       const int r = row0 + wg * CV_TILE + rloc;      // packed row of the request
-      const bool live = r < w.r.n * G;
+      const bool live = r < (w.r.n << p.g_shift);
       // keys [0, lim) are this row's
-      const int lim = !live ? 0 : p.causal ? min(w.r.kv, w.r.kv - w.r.n + r / G + 1) : w.r.kv;
+      const int lim = !live ? 0 : p.causal ? min(w.r.kv, w.r.kv - w.r.n + (r >> p.g_shift) + 1) : w.r.kv;
       const int lim_all = __reduce_min_sync(0xffffffffu, live ? lim : INT32_MAX);
       float mref = -INFINITY, lsum = 0.f;
       for (int u = 0; u < units; ++u, ++j, ++n_s) {
