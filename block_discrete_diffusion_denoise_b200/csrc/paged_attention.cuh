@@ -718,10 +718,10 @@ __global__ void __launch_bounds__(MergeCfg<ROWS>::THREADS) paged_merge_kernel(co
   __shared__ float2 s_ml[ROWS == 16 ? C::THREADS : 1];
   pdl_launch_dependents();
   pdl_wait();
-  // by tile, the first entry says how many there are
-  if (p.cuts_by_tile && static_cast<int>(blockIdx.x) >= p.cuts[0].tiles) return;
+  // by tile, the first entry says how many there are (both are fetched at once)
+  const int tiles = p.cuts[0].tiles;
   const PagedCut cut = p.cuts[blockIdx.x];
-  if (cut.rows == 0) return;
+  if ((p.cuts_by_tile && static_cast<int>(blockIdx.x) >= tiles) || cut.rows == 0) return;
   // items: a row's column group; neighbouring threads take columns of a row where rows lie whole, else rows
   const int items = ROWS == 16 ? cut.rows * (D / 4) : ROWS;
   const int groups = ROWS == 16 ? max(1, C::THREADS / items) : 1;
