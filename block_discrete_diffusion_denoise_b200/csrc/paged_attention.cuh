@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
           // p enters the second product in bf16 (2^-9 of each, averaging out over keys); its sum stays fp32
           const float p0 = ex2_approx(sc[t][2 * x] - base), p1 = ex2_approx(sc[t][2 * x + 1] - base);
           sum += p0 + p1;
-          pf[2 * t + x] = pack_bf16x2(p0, p1);
+          pf[2 * t + x] = cvt_bf16x2(p0, p1);
         }
         l[x] = l[x] * f[x] + sum;
       }
@@ -656,7 +656,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
           const float inv = L == 0.f ? 0.f : 1.f / L;
           const int64_t row = paged_out_row(p, d.t0, d.row0 + r, d.h);
           *reinterpret_cast<uint2*>(p.o + row * D + c4) =
-              make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
+              make_uint2(cvt_bf16x2(a.x * inv, a.y * inv), cvt_bf16x2(a.z * inv, a.w * inv));
           if (p.lse && c4 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
         } else {
           *reinterpret_cast<float4*>(p.part + paged_part_at<TOK_ROWS, D>(slot, r, c4)) = a;
@@ -760,7 +760,7 @@ __global__ void __launch_bounds__(MergeCfg<ROWS>::THREADS) paged_merge_kernel(co
 #pragma unroll
     for (int k = 0; k < C::COLS; ++k)
       *reinterpret_cast<uint2*>(p.o + row * D + c0 + 4 * k) =
-          make_uint2(pack_bf16x2(acc.o[k].x * inv, acc.o[k].y * inv), pack_bf16x2(acc.o[k].z * inv, acc.o[k].w * inv));
+          make_uint2(cvt_bf16x2(acc.o[k].x * inv, acc.o[k].y * inv), cvt_bf16x2(acc.o[k].z * inv, acc.o[k].w * inv));
     if (p.lse && c0 == 0) p.lse[row] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * 0.69314718055994531f;
   }
   if (ROWS == 16 && groups > 1) {
@@ -776,7 +776,7 @@ __global__ void __launch_bounds__(MergeCfg<ROWS>::THREADS) paged_merge_kernel(co
     const float inv = acc.l == 0.f ? 0.f : 1.f / acc.l;
     const int64_t row = paged_out_row(p, cut.t0, cut.row0 + r, cut.h);
     *reinterpret_cast<uint2*>(p.o + row * D + c0) =
-        make_uint2(pack_bf16x2(acc.o[0].x * inv, acc.o[0].y * inv), pack_bf16x2(acc.o[0].z * inv, acc.o[0].w * inv));
+        make_uint2(cvt_bf16x2(acc.o[0].x * inv, acc.o[0].y * inv), cvt_bf16x2(acc.o[0].z * inv, acc.o[0].w * inv));
     if (p.lse && c0 == 0) p.lse[row] = acc.l == 0.f ? -INFINITY : (acc.m + log2f(acc.l)) * 0.69314718055994531f;
   }
 }

@@ -126,13 +126,6 @@ __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
-// two floats to bf16, nearest even, lo in the low half
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
 template <int D>
 __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __grid_constant__ CanvasParams cp) {
   DG_TIMELINE_SCOPE(TLK_ATTENTION);
