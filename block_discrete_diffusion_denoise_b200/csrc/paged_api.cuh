@@ -5,6 +5,7 @@
 #pragma once
 
 #include <atomic>
+#include <initializer_list>
 
 #include "paged.cuh"
 #include "paged_attention.cuh"
@@ -28,6 +29,25 @@ dg_status check_heads(int Hq, int Hkv, int D) {
   if (Hq <= 0 || Hkv <= 0 || D <= 0) return DG_ERR_INVALID_ARG;
   if ((D != 64 && D != 128 && D != 176) || Hq % Hkv || ATC_BQ % (Hq / Hkv) || Hq > 1024) return DG_ERR_UNSUPPORTED;
   return DG_OK;
+}
+
+// a call's operand in device memory
+struct Operand {
+  const void* at;
+  int64_t bytes;
+  bool written;
+};
+
+// Whether some written operand shares memory with another one: other CTAs may
+// still read what it overwrites.
+bool operands_clash(std::initializer_list<Operand> list) {
+  for (const Operand* a = list.begin(); a != list.end(); ++a)
+    for (const Operand* b = a + 1; b != list.end(); ++b) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a->at), y = reinterpret_cast<uintptr_t>(b->at);
+      if ((a->written || b->written) && a->bytes > 0 && b->bytes > 0 && x < y + b->bytes && y < x + a->bytes)
+        return true;
+    }
+  return false;
 }
 
 // a launch's own status; an error that the caller left pending is neither
@@ -202,9 +222,19 @@ dg_status dg_paged_plan(const int32_t* cached, const int32_t* fresh, int32_t bat
       (row_capacity > 0 && (!positions || !slots)))
     return DG_ERR_INVALID_ARG;
   if (shift < 0) return DG_ERR_UNSUPPORTED;
-  // inputs that other CTAs still read must not be outputs
-  if (free_state == free_state_out || cached == kv_lens || fresh == kv_lens) return DG_ERR_INVALID_ARG;
   if (n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;  // a slot is 32 bits
+  const int64_t B = batch;
+  if (operands_clash({{cached, B * 4, false},
+                      {fresh, B * 4, false},
+                      {free_state, 8, false},
+                      {table, ((B - 1) * table_stride + width) * 4, true},
+                      {free_pages, static_cast<int64_t>(n_pages) * 4, true},
+                      {cu_rows, (B + 1) * 4, true},
+                      {kv_lens, B * 4, true},
+                      {positions, static_cast<int64_t>(row_capacity) * 4, true},
+                      {slots, static_cast<int64_t>(row_capacity) * 4, true},
+                      {free_state_out, 16, true}}))
+    return DG_ERR_INVALID_ARG;
   PagedPlanParams p;
   p.cached = cached;
   p.fresh = fresh;
@@ -246,6 +276,15 @@ dg_status dg_paged_append(const void* qkv, int64_t qkv_stride, int32_t n_rows, i
   if (qkv_stride < static_cast<int64_t>(heads) * head_dim || qkv_stride % 8) return DG_ERR_INVALID_ARG;
   if (n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;
   if (n_rows == 0) return DG_OK;
+  const int64_t rows = n_rows, pool = (static_cast<int64_t>(n_pages) << shift) * n_kv_heads * head_dim * 2;
+  if (operands_clash({{qkv, ((rows - 1) * qkv_stride + static_cast<int64_t>(heads) * head_dim) * 2, false},
+                      {positions, rows * 4, false},
+                      {slots, rows * 4, false},
+                      {rope, static_cast<int64_t>(n_positions) * head_dim * 4, false},
+                      {k_pages, pool, true},
+                      {v_pages, pool, true},
+                      {q_out, rows * n_q_heads * head_dim * 2, true}}))
+    return DG_ERR_INVALID_ARG;
   PagedAppendParams p{};
   p.qkv = static_cast<const uint16_t*>(qkv);
   p.qkv_stride = qkv_stride;
@@ -283,6 +322,18 @@ dg_status dg_paged_attention(const dg_paged_attention_args* a, void* cuda_stream
   const bool few = few_rows(a->n_rows, a->max_rows, a->n_q_heads / a->n_kv_heads);
   if (a->workspace_bytes < paged_workspace(few, a->head_dim, sms)) return DG_ERR_CAPACITY;
   const int shift = page_shift_of(a->page_size);
+  const int64_t rows = a->n_rows, width = static_cast<int64_t>(a->n_q_heads) * a->head_dim;
+  const int64_t pool = (static_cast<int64_t>(a->n_pages) << shift) * a->n_kv_heads * a->head_dim * 2;
+  if (operands_clash({{a->q, ((rows - 1) * a->q_stride + width) * 2, false},
+                      {a->k_pages, pool, false},
+                      {a->v_pages, pool, false},
+                      {a->block_table, ((a->batch - 1) * a->table_stride + a->table_width) * 4, false},
+                      {a->kv_lens, a->batch * int64_t(4), false},
+                      {a->cu_rows, (a->batch + int64_t(1)) * 4, false},
+                      {a->out, rows * width * 2, true},
+                      {a->lse, a->lse ? rows * a->n_q_heads * 4 : 0, true},
+                      {a->workspace, paged_workspace(few, a->head_dim, sms), true}}))
+    return DG_ERR_INVALID_ARG;
   CanvasParams cp;
   PagedAttnParams& p = cp.a;
   const uint64_t pool_rows = (static_cast<uint64_t>(a->n_pages) * a->n_kv_heads) << shift;

@@ -271,7 +271,12 @@ __device__ __forceinline__ void paged_list(const PagedAttnParams& p, const Paged
     const int64_t hi = g.q * (c + 1) + min(c + 1, g.more);
     cut.last = paged_holder(g, hi + (w.nb - w.kb1) - 1);
   }
-  if (w.ord < p.cuts_by_tile) p.cuts[w.ord] = cut;   // more only where cu_rows decreases
+  if (static_cast<uint32_t>(w.ord) < static_cast<uint32_t>(p.cuts_by_tile)) p.cuts[w.ord] = cut;
+}
+
+// A list by tile of a call without tiles: its first entry says so.
+__device__ __forceinline__ void paged_list_none(const PagedAttnParams& p, const PagedRange& g) {
+  if (g.tiles == 0 && p.cuts_by_tile && blockIdx.x == 0 && threadIdx.x == 0) p.cuts[0] = PagedCut{};
 }
 
 // untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
@@ -422,6 +427,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
   }
   pdl_wait();
   const PagedRange g = paged_range<TOK_ROWS, TOK_THREADS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
+  paged_list_none(p, g);
   bool ok = true;
 
   if (warp == 0) {

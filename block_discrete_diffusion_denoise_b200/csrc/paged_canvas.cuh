@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   tc_fence_before();
   pdl_wait();
   const PagedRange g = paged_range<CV_ROWS, CV_THREADS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
+  paged_list_none(p, g);
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   bool ok = true;

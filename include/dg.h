@@ -444,7 +444,11 @@ dg_status dg_lmhead_argmax_static(const void* z_dev, int32_t n_rows, int32_t d_m
  * and reports only its own launches' status.  Lengths and tables are read on
  * the device, so a captured call may be replayed with others.  Index values
  * from device memory are checked there: an id or a length that is out of range
- * is never followed (what it does instead stands at each call).
+ * is never followed (what it does instead stands at each call).  Memory that a
+ * call writes must not overlap any other of its operands
+ * (DG_ERR_INVALID_ARG).  The first call on a device looks up its size and sets
+ * the kernels' attributes: make it before any capture; first calls may come
+ * from any thread.
  * ------------------------------------------------------------------------- */
 
 /* Block tables, slots and positions of a call's new rows, from the requests'
@@ -469,8 +473,9 @@ dg_status dg_lmhead_argmax_static(const void* z_dev, int32_t n_rows, int32_t d_m
  * reason is set (bit 0: a negative length, or new < -cached; bit 1: a request
  * needs more than table_width pages; bit 2: more than row_capacity rows; bit
  * 3: free_state is no state of the ring), no page changes hands, kv_lens
- * is cached and the rows' slots are -1, which dg_paged_append skips.
- * free_state_out_dev must not be free_state_dev, nor kv_lens_dev an input. */
+ * is cached and the rows' slots are -1, which dg_paged_append skips.  A call
+ * leaves free_state_dev as it was, so it may be made again, or its outcome be
+ * dropped, until the next one is given its free_state_out_dev. */
 dg_status dg_paged_plan(const int32_t* cached_dev, const int32_t* new_dev, int32_t batch, int32_t* block_table_dev,
                         int32_t table_width, int64_t table_stride, int32_t* free_pages_dev, int32_t n_pages,
                         const int32_t* free_state_dev, int32_t page_size, int32_t* cu_rows_dev,

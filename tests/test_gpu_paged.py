@@ -346,6 +346,31 @@ def test_attention_leaves_rows_outside_the_requests(rows):
         assert (out[edge] == 4).all() and (lse[edge] == 4).all()
 
 
+@pytest.mark.parametrize("batch", [1, 300])
+@pytest.mark.parametrize("rows", [1, 600])
+def test_attention_of_rows_that_belong_to_no_request(batch, rows):
+    """no request has a row: nothing is written, whatever the workspace held"""
+    g = torch.Generator().manual_seed(20)
+    q, k, v, table, cu = paged_cache(g, TINY, 16, [40] * batch, [0] * batch)
+    q = torch.randn(rows, 4, 64, generator=g).to(BF).cuda()
+    out = torch.full_like(q, 4.0)
+    lse = torch.full((rows, 4), 4.0, device="cuda")
+    for fill in (0x7f, 0x01):
+        torch.full((64 << 20,), fill, dtype=torch.uint8, device="cuda")          # freed: the workspace's next memory
+        dg.paged_attention(q, k.cuda(), v.cuda(), table.cuda(), i32([40] * batch), i32(cu), out, lse=lse)
+    assert (out == 4).all() and (lse == 4).all()
+
+
+def test_attention_refuses_memory_that_it_would_overwrite():
+    g = torch.Generator().manual_seed(21)
+    q, k, v, table, cu = paged_cache(g, SMALL, 16, [40], [20])
+    a = [t.cuda() for t in (q, k, v, table)]
+    for out in (a[0], a[1].view(-1)[:20 * 8 * 128].view(20, 8, 128)):
+        with pytest.raises(dg.DGError) as e:
+            dg.paged_attention(*a, i32([40]), i32(cu), out)
+        assert e.value.status == dg.DG_ERR_INVALID_ARG
+
+
 @pytest.mark.parametrize("rows", [1, 40])
 def test_attention_with_large_scores_and_values(rows):
     """scores far from zero in both directions, and one key that takes all the weight"""

@@ -47,6 +47,8 @@ def plan(**kw):
     (dict(cu=None), 1), (dict(kv=None), 1), (dict(out=None), 1), (dict(pos=None), 1), (dict(slots=None), 1),
     (dict(batch=0), 1), (dict(batch=-1), 1), (dict(width=0), 1), (dict(stride=7), 1), (dict(n_pages=0), 1),
     (dict(cap=-1), 1), (dict(out=A + 0x4000), 1), (dict(kv=A), 1), (dict(kv=A + 0x1000), 1),
+    (dict(out=A + 0x4000 - 8), 1), (dict(slots=A + 0x7000), 1), (dict(slots=A + 0x7000 + 36), 1), (dict(cu=A + 8), 1),
+    (dict(ring=A + 0x2000 + 4 * 23), 1), (dict(pos=A + 0x3000 + 4 * 99), 1),
     (dict(page=0), 7), (dict(page=48), 7), (dict(page=256), 7), (dict(n_pages=2 ** 31 // 64), 3),
 ])
 def test_plan_refuses(kw, status):
@@ -54,8 +56,8 @@ def test_plan_refuses(kw, status):
 
 
 def append(**kw):
-    a = dict(qkv=A, stride=5632, rows=4, hq=16, hkv=8, d=176, pos=A + 0x1000, slots=A + 0x2000, rope=A + 0x3000,
-             n_pos=100, k=A + 0x4000, v=A + 0x5000, n_pages=10, page=64, q=A + 0x6000)
+    a = dict(qkv=A, stride=5632, rows=4, hq=16, hkv=8, d=176, pos=A + 0x20000, slots=A + 0x21000, rope=A + 0x22000,
+             n_pos=100, k=A + 0x1000000, v=A + 0x2000000, n_pages=10, page=64, q=A + 0x40000)
     a.update(kw)
     return dg.load_library().dg_paged_append(a["qkv"], a["stride"], a["rows"], a["hq"], a["hkv"], a["d"], a["pos"],
                                              a["slots"], a["rope"], a["n_pos"], a["k"], a["v"], a["n_pages"], a["page"],
@@ -68,6 +70,8 @@ def append(**kw):
     (dict(qkv=A + 8), 1), (dict(rope=A + 4), 1), (dict(k=A + 2), 1), (dict(v=A + 8), 1), (dict(q=A + 8), 1),
     (dict(stride=5631), 1), (dict(stride=5636), 1), (dict(hq=0), 1), (dict(d=96, stride=5632), 7), (dict(hkv=3), 7),
     (dict(hq=24, stride=8000), 7), (dict(page=17), 7), (dict(n_pages=2 ** 25), 3), (dict(rows=0), 0),
+    (dict(q=A), 1), (dict(q=A + 4 * 5632 * 2 - 16), 1), (dict(v=A + 0x1000000), 1), (dict(k=A + 0x20000), 1),
+    (dict(v=A + 0x1000000 + 10 * 64 * 8 * 176 * 2 - 16), 1),
 ])
 def test_append_refuses(kw, status):
     assert append(**kw) == status
