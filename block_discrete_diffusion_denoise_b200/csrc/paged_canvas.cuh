@@ -390,9 +390,11 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
         if (lane == 0) mbar_arrive(&s_free[wg]);
         if (key0 + PG_BK > lim_all || valid != ~uint64_t(0)) {
           const int lj = lim - key0;
+          const uint64_t seen = lj >= PG_BK ? valid : lj <= 0 ? 0 : valid & ((uint64_t(1) << lj) - 1);
+          const uint32_t half[2] = {static_cast<uint32_t>(seen), static_cast<uint32_t>(seen >> 32)};
 #pragma unroll
           for (int c = 0; c < PG_BK; ++c)
-            if (c >= lj || !(valid >> c & 1)) s[c] = -INFINITY;
+            if (!(half[c / 32] & (1u << (c % 32)))) s[c] = -INFINITY;
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
