@@ -506,9 +506,22 @@ def lmhead_argmax_static(z, embed, temperature, argmax=None, lse=None, conf=None
 # workspace of an attention call; arguments are checked first, and a bad one
 # raises DGError with nothing launched.
 #
-# A call's host time counts (its kernels take a few microseconds), so a good
-# operand is told by four attribute reads and the messages are made for a bad
-# one only.
+# A call's host time counts (its kernels take a few microseconds), so the
+# conditions of a good call are one expression over attribute reads, with what
+# torch offers bound to module names; what is wrong with a bad one is found
+# again, condition by condition, in order to say it.
+_BF16 = _I32 = _F32 = _current_device = _raw_stream = None
+
+
+def _bind_torch():
+    """torch, imported by the first call (importing this package does not need it)."""
+    global _BF16, _I32, _F32, _current_device, _raw_stream
+    import torch
+    load_library()
+    _BF16, _I32, _F32 = torch.bfloat16, torch.int32, torch.float32
+    # torch.cuda.current_stream() makes an object of what these two tell
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
 
 def _paged_bad(t, what, want):
     got = f"{t.dtype} {tuple(t.shape)} on {t.device}{'' if t.is_contiguous() else ' (strided)'}" \
@@ -516,53 +529,42 @@ def _paged_bad(t, what, want):
     _invalid(f"{what}: expected {want}, got {got}")
 
 
-def _paged_ints(t, n, what, i32, idx):
-    """Address of t: a contiguous int32 tensor of at least n elements on CUDA device idx."""
-    try:
-        if t.dtype is i32 and t.get_device() == idx and t.numel() >= n and t.is_contiguous():
-            return t.data_ptr()
-    except AttributeError:
-        pass
-    _paged_bad(t, what, f"a contiguous int32 tensor of at least {n} elements on cuda:{idx}")
+def _paged_check_ints(t, n, what, idx):
+    if not (hasattr(t, "get_device") and t.dtype is _I32 and t.get_device() == idx and t.numel() >= n
+            and t.is_contiguous()):
+        _paged_bad(t, what, f"a contiguous int32 tensor of at least {n} elements on cuda:{idx}")
 
 
-def _paged_operand(t, dtype, ndim, what):
-    """CUDA device index of t, a tensor of `dtype` with `ndim` dimensions."""
-    idx = t.get_device() if hasattr(t, "get_device") else -1
-    if idx < 0 or t.dtype is not dtype or t.dim() != ndim:
-        _paged_bad(t, what, f"a {ndim}-dimensional CUDA tensor of {dtype}")
-    return idx
+def _paged_check(t, dtype, what, want, idx=None, ndim=None, shape=None, dense=True):
+    """Refuse t unless it is a CUDA tensor of `dtype` (on device idx, with ndim dimensions or the shape, contiguous)."""
+    if not (hasattr(t, "get_device") and t.dtype is dtype and t.get_device() >= 0
+            and (idx is None or t.get_device() == idx) and (ndim is None or t.dim() == ndim)
+            and (shape is None or tuple(t.shape) == tuple(shape)) and (not dense or t.is_contiguous())):
+        _paged_bad(t, what, f"{want}{'' if idx is None else f' on cuda:{idx}'}")
 
 
-def _paged_table(t, i32, idx):
-    """(batch, width, row stride) of a block table on CUDA device idx (None: its own)."""
-    own = _paged_operand(t, i32, 2, "block_table")
-    B, W = t.shape
-    if (idx is not None and own != idx) or W < 1 or (t.stride(1) != 1 and W > 1):
-        _paged_bad(t, "block_table", f"a [batch, width] int32 tensor with adjacent entries on cuda:{idx}")
-    return B, W, (t.stride(0) if B > 1 else W)
+def _paged_check_table(t, idx):
+    _paged_check(t, _I32, "block_table", "a [batch, width] int32 tensor with adjacent entries", idx, 2, dense=False)
+    if t.shape[1] < 1 or (t.stride(1) != 1 and t.shape[1] > 1):
+        _paged_bad(t, "block_table", "a [batch, width] int32 tensor with adjacent entries")
 
 
-def _paged_pools(k_pages, v_pages, bf16, idx):
-    for t, what in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if _paged_operand(t, bf16, 4, what) != idx or not t.is_contiguous():
-            _paged_bad(t, what, f"a contiguous [n_pages, n_kv_heads, page_size, head_dim] bf16 tensor on cuda:{idx}")
-    shape = k_pages.shape
-    if shape != v_pages.shape:
-        _invalid(f"k_pages {tuple(shape)} and v_pages {tuple(v_pages.shape)} differ")
-    return shape
+def _paged_check_pools(k_pages, v_pages, idx):
+    want = "a contiguous [n_pages, n_kv_heads, page_size, head_dim] bfloat16 tensor"
+    _paged_check(k_pages, _BF16, "k_pages", want, idx, 4)
+    _paged_check(v_pages, _BF16, "v_pages", want + " like k_pages", idx, shape=k_pages.shape)
 
 
-def _paged_call(name, idx, *args):
-    """The call with CUDA device idx current, its stream torch's current one there."""
-    import torch
-    c = torch._C                      # torch.cuda.current_stream() makes an object of what these two tell
-    if c._cuda_getDevice() != idx:
+def _paged_call(f, idx, *args):
+    """The library's f with CUDA device idx current, on torch's current stream there."""
+    if _current_device() == idx:
+        st = f(*args, _raw_stream(idx))
+    else:
+        import torch
         with torch.cuda.device(idx):
-            return _paged_call(name, idx, *args)
-    st = getattr(_lib or load_library(), name)(*args, c._cuda_getCurrentRawStream(idx))
+            st = f(*args, _raw_stream(idx))
     if st != DG_OK:
-        raise DGError(st, f"{name} refused (shape, alignment or capacity; see include/dg.h)")
+        raise DGError(st, f"{f.__name__} refused (shape, alignment, overlap or capacity; see include/dg.h)")
 
 
 def rope_table(n_positions: int, head_dim: int, base: float = 10000.0, device="cuda"):
@@ -583,21 +585,45 @@ def paged_plan(cached_lens, new_rows, block_table, free_pages, free_state, page_
     [batch + 1], kv_lens [batch], positions and slots [row capacity] and
     free_state_out [4] are written; free_state [>= 2] is read (pass the last
     call's free_state_out, and another buffer to write)."""
-    import torch
-    i32 = torch.int32
-    idx = _paged_operand(block_table, i32, 2, "block_table")
-    B, W, stride = _paged_table(block_table, i32, idx)
-    ring = _paged_ints(free_pages, 1, "free_pages", i32, idx)
-    rows = _paged_ints(slots, 0, "slots", i32, idx)
-    cap = slots.numel()
-    if B == 0:
-        _invalid("block_table: no request")
-    _paged_call("dg_paged_plan", idx, _paged_ints(cached_lens, B, "cached_lens", i32, idx),
-                _paged_ints(new_rows, B, "new_rows", i32, idx), B, block_table.data_ptr(), W, stride, ring,
-                free_pages.numel(), _paged_ints(free_state, 2, "free_state", i32, idx), page_size,
-                _paged_ints(cu_rows, B + 1, "cu_rows", i32, idx), _paged_ints(kv_lens, B, "kv_lens", i32, idx),
-                _paged_ints(positions, cap, "positions", i32, idx), rows, cap,
-                _paged_ints(free_state_out, 4, "free_state_out", i32, idx))
+    if _I32 is None:
+        _bind_torch()
+    i32 = _I32
+    try:
+        B, W = block_table.shape
+        cap = slots.numel()
+        idx = block_table.get_device()
+        good = (idx >= 0 and B > 0 and W > 0 and block_table.dtype is i32
+                and cached_lens.dtype is i32 and cached_lens.get_device() == idx and cached_lens.numel() >= B
+                and new_rows.dtype is i32 and new_rows.get_device() == idx and new_rows.numel() >= B
+                and free_pages.dtype is i32 and free_pages.get_device() == idx
+                and free_state.dtype is i32 and free_state.get_device() == idx and free_state.numel() >= 2
+                and cu_rows.dtype is i32 and cu_rows.get_device() == idx and cu_rows.numel() > B
+                and kv_lens.dtype is i32 and kv_lens.get_device() == idx and kv_lens.numel() >= B
+                and positions.dtype is i32 and positions.get_device() == idx and positions.numel() >= cap
+                and slots.dtype is i32 and slots.get_device() == idx
+                and free_state_out.dtype is i32 and free_state_out.get_device() == idx and free_state_out.numel() >= 4
+                and cached_lens.is_contiguous() and new_rows.is_contiguous() and free_pages.is_contiguous()
+                and free_state.is_contiguous() and cu_rows.is_contiguous() and kv_lens.is_contiguous()
+                and positions.is_contiguous() and slots.is_contiguous() and free_state_out.is_contiguous())
+        stride = W if block_table.is_contiguous() else block_table.stride(0)
+        good = good and (stride == W or block_table.stride(1) == 1 or W == 1)
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        _paged_check_table(block_table, None)
+        B, idx = block_table.shape[0], block_table.get_device()
+        if B == 0:
+            _invalid("block_table: no request")
+        _paged_check_ints(slots, 0, "slots", idx)
+        for t, n, what in ((cached_lens, B, "cached_lens"), (new_rows, B, "new_rows"), (free_pages, 1, "free_pages"),
+                           (free_state, 2, "free_state"), (cu_rows, B + 1, "cu_rows"), (kv_lens, B, "kv_lens"),
+                           (positions, slots.numel(), "positions"), (free_state_out, 4, "free_state_out")):
+            _paged_check_ints(t, n, what, idx)
+        _invalid("arguments")
+    _paged_call(_lib.dg_paged_plan, idx, cached_lens.data_ptr(), new_rows.data_ptr(), B, block_table.data_ptr(), W,
+                stride if B > 1 else W, free_pages.data_ptr(), free_pages.numel(), free_state.data_ptr(), page_size,
+                cu_rows.data_ptr(), kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), cap,
+                free_state_out.data_ptr())
 
 
 def paged_append(qkv, positions, slots, rope, k_pages, v_pages, q_out):
@@ -606,28 +632,51 @@ def paged_append(qkv, positions, slots, rope, k_pages, v_pages, q_out):
     [rows, Hq, D], k and v to `slots` of the pages [n_pages, Hkv, page_size,
     D].  positions and slots (int32) hold at least `rows` entries; rope is
     rope_table's."""
-    import torch
-    bf16, i32 = torch.bfloat16, torch.int32
-    idx = _paged_operand(qkv, bf16, 2, "qkv")
-    rows, width = qkv.shape
-    n_pages, hkv, page, d = _paged_pools(k_pages, v_pages, bf16, idx)
-    if _paged_operand(q_out, bf16, 3, "q_out") != idx or not q_out.is_contiguous():
-        _paged_bad(q_out, "q_out", f"a contiguous [{rows}, Hq, {d}] bf16 tensor on cuda:{idx}")
-    n, hq, dq = q_out.shape
-    if n != rows or dq != d:
-        _paged_bad(q_out, "q_out", f"a contiguous [{rows}, Hq, {d}] bf16 tensor on cuda:{idx}")
-    if width != (hq + 2 * hkv) * d or (qkv.stride(1) != 1 and rows):
-        _paged_bad(qkv, "qkv", f"rows of {(hq + 2 * hkv) * d} adjacent elements")
-    if _paged_operand(rope, torch.float32, 3, "rope") != idx or not rope.is_contiguous() \
-            or rope.shape[1:] != (d // 2, 2):
-        _paged_bad(rope, "rope", f"a contiguous [positions, {d // 2}, 2] float32 tensor on cuda:{idx}")
-    pos = _paged_ints(positions, rows, "positions", i32, idx)
-    at = _paged_ints(slots, rows, "slots", i32, idx)
+    if _I32 is None:
+        _bind_torch()
+    bf16, i32 = _BF16, _I32
+    try:
+        rows, width = qkv.shape
+        n_pages, hkv, page, d = pool = k_pages.shape
+        n, hq, dq = q_out.shape
+        n_pos, half, two = rope.shape
+        idx = qkv.get_device()
+        good = (idx >= 0 and qkv.dtype is bf16 and n == rows and dq == d and width == (hq + 2 * hkv) * d
+                and half * 2 == d and two == 2
+                and k_pages.dtype is bf16 and k_pages.get_device() == idx and k_pages.is_contiguous()
+                and v_pages.dtype is bf16 and v_pages.get_device() == idx and v_pages.is_contiguous()
+                and v_pages.shape == pool
+                and q_out.dtype is bf16 and q_out.get_device() == idx and q_out.is_contiguous()
+                and rope.dtype is _F32 and rope.get_device() == idx and rope.is_contiguous()
+                and positions.dtype is i32 and positions.get_device() == idx and positions.numel() >= rows
+                and positions.is_contiguous()
+                and slots.dtype is i32 and slots.get_device() == idx and slots.numel() >= rows
+                and slots.is_contiguous())
+        stride = width if qkv.is_contiguous() else qkv.stride(0)
+        good = good and (stride == width or qkv.stride(1) == 1)
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        _paged_check(qkv, bf16, "qkv", "a [rows, (Hq + 2 Hkv) * D] bfloat16 tensor", None, 2, dense=False)
+        rows, idx = qkv.shape[0], qkv.get_device()
+        _paged_check_pools(k_pages, v_pages, idx)
+        hkv, d = k_pages.shape[1], k_pages.shape[3]
+        want = f"a contiguous [{rows}, Hq, {d}] bfloat16 tensor"
+        _paged_check(q_out, bf16, "q_out", want, idx, 3)
+        _paged_check(q_out, bf16, "q_out", want, idx, shape=(rows, q_out.shape[1], d))
+        if qkv.shape[1] != (q_out.shape[1] + 2 * hkv) * d or qkv.stride(1) != 1:
+            _paged_bad(qkv, "qkv", f"rows of {(q_out.shape[1] + 2 * hkv) * d} adjacent elements")
+        want = f"a contiguous [positions, {d // 2}, 2] float32 tensor"
+        _paged_check(rope, _F32, "rope", want, idx, 3)
+        _paged_check(rope, _F32, "rope", want, idx, shape=(rope.shape[0], d // 2, 2))
+        _paged_check_ints(positions, rows, "positions", idx)
+        _paged_check_ints(slots, rows, "slots", idx)
+        _invalid("arguments")
     if rows == 0:
         return
-    _paged_call("dg_paged_append", idx, qkv.data_ptr(), qkv.stride(0) if rows > 1 else width, rows, hq, hkv, d, pos,
-                at, rope.data_ptr(), rope.shape[0], k_pages.data_ptr(), v_pages.data_ptr(), n_pages, page,
-                q_out.data_ptr())
+    _paged_call(_lib.dg_paged_append, idx, qkv.data_ptr(), stride if rows > 1 else width, rows, hq, hkv, d,
+                positions.data_ptr(), slots.data_ptr(), rope.data_ptr(), n_pos, k_pages.data_ptr(), v_pages.data_ptr(),
+                n_pages, page, q_out.data_ptr())
 
 
 _PAGED_ATTENTION_ARGS = struct.Struct("@9P3q10if4x")     # dg_paged_attention_args
@@ -644,46 +693,79 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_lens, cu_rows, out, lse
     the n new rows being the request's last; else all of them.  max_rows is an
     upper bound of a request's rows where the caller knows one (it picks the
     kernel); scale defaults to D ** -0.5."""
-    import torch
-    bf16, i32 = torch.bfloat16, torch.int32
-    idx = _paged_operand(q, bf16, 3, "q")
-    shape = q.shape
-    rows, hq, d = shape
-    n_pages, hkv, page, dk = _paged_pools(k_pages, v_pages, bf16, idx)
-    if dk != d or (rows and (q.stride(2) != 1 or q.stride(1) != d)):
-        _paged_bad(q, "q", f"[rows, Hq, {dk}] with adjacent heads")
-    if _paged_operand(out, bf16, 3, "out") != idx or out.shape != shape or not out.is_contiguous():
-        _paged_bad(out, "out", f"a contiguous {tuple(shape)} bf16 tensor on cuda:{idx}")
-    lse_at = 0
-    if lse is not None:
-        if _paged_operand(lse, torch.float32, 2, "lse") != idx or lse.shape != (rows, hq) or not lse.is_contiguous():
-            _paged_bad(lse, "lse", f"a contiguous {(rows, hq)} float32 tensor on cuda:{idx}")
-        lse_at = lse.data_ptr()
-    B, W, stride = _paged_table(block_table, i32, idx)
-    kv = _paged_ints(kv_lens, B, "kv_lens", i32, idx)
-    cu = _paged_ints(cu_rows, B + 1, "cu_rows", i32, idx)
+    if _I32 is None:
+        _bind_torch()
+    bf16, i32 = _BF16, _I32
+    try:
+        rows, hq, d = shape = q.shape
+        n_pages, hkv, page, dk = pool = k_pages.shape
+        B, W = block_table.shape
+        idx = q.get_device()
+        good = (idx >= 0 and q.dtype is bf16 and dk == d and W > 0
+                and k_pages.dtype is bf16 and k_pages.get_device() == idx and k_pages.is_contiguous()
+                and v_pages.dtype is bf16 and v_pages.get_device() == idx and v_pages.is_contiguous()
+                and v_pages.shape == pool
+                and out.dtype is bf16 and out.get_device() == idx and out.is_contiguous() and out.shape == shape
+                and block_table.dtype is i32 and block_table.get_device() == idx
+                and kv_lens.dtype is i32 and kv_lens.get_device() == idx and kv_lens.numel() >= B
+                and kv_lens.is_contiguous()
+                and cu_rows.dtype is i32 and cu_rows.get_device() == idx and cu_rows.numel() > B
+                and cu_rows.is_contiguous())
+        if lse is None:
+            lse_at = 0
+        else:
+            good = good and (lse.dtype is _F32 and lse.get_device() == idx and lse.is_contiguous()
+                             and lse.shape == (rows, hq))
+            lse_at = lse.data_ptr()
+        if q.is_contiguous():
+            q_stride = hq * d
+        else:
+            q_stride = q.stride(0)
+            good = good and q.stride(2) == 1 and q.stride(1) == d
+        stride = W if block_table.is_contiguous() else block_table.stride(0)
+        good = good and (stride == W or block_table.stride(1) == 1 or W == 1)
+    except (AttributeError, ValueError):
+        good = False
+    if not good:
+        _paged_check(q, bf16, "q", "a [rows, Hq, D] bfloat16 tensor with adjacent heads", None, 3, dense=False)
+        (rows, hq, d), idx = q.shape, q.get_device()
+        if rows and (q.stride(2) != 1 or q.stride(1) != d):
+            _paged_bad(q, "q", "a [rows, Hq, D] bfloat16 tensor with adjacent heads")
+        _paged_check_pools(k_pages, v_pages, idx)
+        if k_pages.shape[3] != d:
+            _paged_bad(q, "q", f"[rows, Hq, {k_pages.shape[3]}], the pages' head_dim")
+        _paged_check(out, bf16, "out", f"a contiguous {tuple(q.shape)} bfloat16 tensor", idx, shape=q.shape)
+        if lse is not None:
+            _paged_check(lse, _F32, "lse", f"a contiguous {(rows, hq)} float32 tensor", idx, shape=(rows, hq))
+        _paged_check_table(block_table, idx)
+        _paged_check_ints(kv_lens, block_table.shape[0], "kv_lens", idx)
+        _paged_check_ints(cu_rows, block_table.shape[0] + 1, "cu_rows", idx)
+        _invalid("arguments")
     if rows == 0 or B == 0:
         return
-    max_rows = int(max_rows)
-    if hq % hkv:
+    if hkv == 0 or hq % hkv:
         raise DGError(DG_ERR_UNSUPPORTED, f"{hq} query heads on {hkv} kv heads")
-    head = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), kv, cu, out.data_ptr(), lse_at)
-    tail = (q.stride(0) if rows > 1 else hq * d, stride, rows, B, hq, hkv, d, n_pages, page, W, 1 if causal else 0,
-            max_rows, d ** -0.5 if scale is None else scale)
-    # its size goes by the device and these numbers alone, and all bounds of over 16 rows are alike
+    # its workspace's size goes by the device and these numbers alone, and all bounds of over 16 rows are alike
     key = (idx, d, hq // hkv, min(max_rows if 0 < max_rows < rows else rows, 17))
-    need = _paged_workspace_bytes.get(key)
-    if need is None:
-        n = ctypes.c_int64()
-        with torch.cuda.device(idx):
-            st = load_library().dg_paged_attention_workspace(_PAGED_ATTENTION_ARGS.pack(*head, 0, 0, *tail),
-                                                             ctypes.byref(n))
-        if st != DG_OK:
-            raise DGError(st, "dg_paged_attention refused (shape, alignment or capacity; see include/dg.h)")
-        need = _paged_workspace_bytes[key] = n.value
-    # from torch's allocator: calls on other streams and in other graphs get memory of their own
-    ws = q.new_empty(need // 2)
-    _paged_call("dg_paged_attention", idx, _PAGED_ATTENTION_ARGS.pack(*head, ws.data_ptr(), need, *tail))
+    need = _paged_workspace_bytes.get(key, 0)
+    if need:
+        # from torch's allocator: calls on other streams and in other graphs get memory of their own
+        ws = q.new_empty(need // 2)
+    args = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
+            cu_rows.data_ptr(), out.data_ptr(), lse_at, ws.data_ptr() if need else 0, need,
+            q_stride if rows > 1 else hq * d, stride if B > 1 else W, rows, B, hq, hkv, d, n_pages, page, W,
+            1 if causal else 0, max_rows, d ** -0.5 if scale is None else scale)
+    if need:
+        _paged_call(_lib.dg_paged_attention, idx, _PAGED_ATTENTION_ARGS.pack(*args))
+        return
+    n = ctypes.c_int64()
+    import torch
+    with torch.cuda.device(idx):
+        st = _lib.dg_paged_attention_workspace(_PAGED_ATTENTION_ARGS.pack(*args), ctypes.byref(n))
+    if st != DG_OK:
+        raise DGError(st, "dg_paged_attention refused (shape, alignment or capacity; see include/dg.h)")
+    _paged_workspace_bytes[key] = n.value
+    paged_attention(q, k_pages, v_pages, block_table, kv_lens, cu_rows, out, lse, causal, max_rows, scale)
 
 
 def anneal_temperature(step: int, max_steps: int = 48, t_first: float = 0.8, t_last: float = 0.4) -> float:

@@ -432,6 +432,65 @@ def test_attention_is_the_same_every_time(rows):
 
 
 # ---------------------------------------------------------------------------
+# what the binding refuses
+# ---------------------------------------------------------------------------
+def refusals(fn, good, bad):
+    """fn takes the good arguments; each of the bad ones in an argument's place is refused, with its name said"""
+    fn(**good)
+    for name, values in bad.items():
+        for v in values:
+            with pytest.raises(dg.DGError) as e:
+                fn(**{**good, name: v})
+            assert e.value.status == dg.DG_ERR_INVALID_ARG and (name in str(e.value) or "q" in str(e.value)), (name, e.value)
+    torch.cuda.synchronize()
+
+
+def misfits(t, shorter=True):
+    """t on the host, of another type, strided, and one element short"""
+    wide = torch.stack([t, t], -1)[..., 0]
+    return [t.cpu(), t.double(), wide if t.numel() > 1 else t.cpu(), None] + \
+        ([t[:-1]] if shorter and t.dim() == 1 else [])
+
+
+def test_plan_refuses_misfits():
+    good = dict(cached_lens=i32([5, 70]), new_rows=i32([3, 1]), block_table=i32([[0, -1], [1, 2]]),
+                free_pages=i32(range(9)), free_state=i32([3, 6]), page_size=64, cu_rows=i32([0] * 3), kv_lens=i32([0] * 2),
+                positions=i32([0] * 8), slots=i32([0] * 8), free_state_out=i32([0] * 4))
+    bad = {k: misfits(v, k not in ("free_pages", "slots")) for k, v in good.items() if k not in ("page_size", "block_table")}
+    bad["block_table"] = [good["block_table"].cpu(), good["block_table"].long(), i32([0, 1]), i32([[0, 1], [2, 3]]).t(),
+                          None, i32([[], []])]
+    refusals(dg.paged_plan, good, bad)
+    with pytest.raises(dg.DGError) as e:
+        dg.paged_plan(**{**good, "page_size": 48})
+    assert e.value.status == dg.DG_ERR_UNSUPPORTED
+
+
+def test_append_refuses_misfits():
+    good = dict(qkv=torch.zeros(4, 512, dtype=BF, device="cuda"), positions=i32([0] * 4), slots=i32(range(4)),
+                rope=dg.rope_table(10, 64), k_pages=torch.zeros(2, 2, 16, 64, dtype=BF, device="cuda"),
+                v_pages=torch.zeros(2, 2, 16, 64, dtype=BF, device="cuda"),
+                q_out=torch.zeros(4, 4, 64, dtype=BF, device="cuda"))
+    bad = {k: misfits(v) for k, v in good.items()}
+    bad["qkv"] += [good["qkv"][:3], torch.zeros(4, 448, dtype=BF, device="cuda")]
+    bad["rope"] += [dg.rope_table(10, 128)]
+    bad["v_pages"] += [torch.zeros(3, 2, 16, 64, dtype=BF, device="cuda")]
+    refusals(dg.paged_append, good, bad)
+
+
+def test_attention_refuses_misfits():
+    good = dict(q=torch.zeros(4, 4, 64, dtype=BF, device="cuda"), k_pages=torch.zeros(2, 2, 16, 64, dtype=BF, device="cuda"),
+                v_pages=torch.zeros(2, 2, 16, 64, dtype=BF, device="cuda"), block_table=i32([[0, 1], [1, 0]]),
+                kv_lens=i32([20, 3]), cu_rows=i32([0, 2, 4]), out=torch.zeros(4, 4, 64, dtype=BF, device="cuda"),
+                lse=torch.zeros(4, 4, device="cuda"))
+    bad = {k: misfits(v) for k, v in good.items() if k != "block_table"}
+    bad["lse"] = [x for x in bad["lse"] if x is not None] + [torch.zeros(4, 5, device="cuda")]
+    bad["out"] += [good["out"][:3]]
+    bad["q"] += [torch.zeros(4, 4, 128, dtype=BF, device="cuda")]
+    bad["block_table"] = [good["block_table"].cpu(), good["block_table"].long(), i32([0, 1]), i32([[0, 1], [2, 3]]).t(), None]
+    refusals(dg.paged_attention, good, bad)
+
+
+# ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
 class Server:

@@ -114,3 +114,5 @@ def test_the_binding_refuses_host_tensors():
     refused(dg.paged_plan, i, i, i.view(2, 2), i, i, 16, i, i, i, i, i)
     refused(dg.paged_append, b.view(4, -1), i, i, torch.zeros(4, 32, 2), pool, pool, b)
     refused(dg.paged_attention, b, pool, pool, i.view(2, 2), i, i, b)
+    refused(dg.paged_attention, None, pool, pool, i.view(2, 2), i, i, b)
+    refused(dg.paged_plan, None, i, None, i, i, 16, i, i, i, i, i)
