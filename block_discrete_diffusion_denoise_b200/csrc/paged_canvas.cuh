@@ -11,7 +11,12 @@
 // that is ready, 30 for a commit, 2800 for a unit.)  The warps are a
 // persistent pipeline over the CTA's stretch of units (paged_attention.cuh);
 // each role walks it by itself, and a word per unit tells the softmax warps
-// which keys the producers found.
+// which keys the producers found.  At D = 176 a unit's products take 1777
+// cycles (48.6 per k-step of S, where both operands come from shared memory and
+// Q is read again for each, 88.5 of P V) and a unit 2050 to 2100.  A canvas of
+// 256 rows over 33,024 keys, 16/8 heads of 176: 97 us with the merge, 980
+// TFLOP/s (114 us once the power limit lowers the clock); eight canvases over
+// 1.5k..6.5k keys 116 us; one over 2304 keys 21.8 us.
 #pragma once
 
 #include "paged_attention.cuh"

@@ -514,7 +514,7 @@ class Server:
         dg.paged_plan(self.cached, new, self.table, self.ring, self.state[0], self.page, self.cu, self.kv, self.pos,
                       self.slot, self.state[1])
         self.state.reverse()
-        q = torch.empty(qkv.shape[0], hq, d, dtype=BF, device="cuda")
+        self.q = q = torch.empty(qkv.shape[0], hq, d, dtype=BF, device="cuda")
         out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
         dg.paged_append(qkv, self.pos, self.slot, self.rope, self.k, self.v, q)
         dg.paged_attention(q, self.k, self.v, self.table, self.kv, self.cu, out, lse=lse, causal=causal,
@@ -523,24 +523,21 @@ class Server:
         return out, lse
 
 
-def contiguous(heads, history, n_new, causal):
-    """attention of one request from its whole history of qkv rows (bf16, CPU), in 64 bits with the
-    roundings of the stored q and k"""
+def rotated(heads, history):
+    """(rows, bound) of the q and k heads of one request's whole history of qkv rows, in 64 bits"""
     hq, hkv, d = heads
     x = history.double().view(-1, hq + 2 * hkv, d)
-    n = x.shape[0]
     j = torch.arange(d // 2, dtype=torch.float64)
-    a = torch.arange(n, dtype=torch.float64)[:, None] * 10000.0 ** (-2 * j / d)
-    y, _ = ref.rotate(x[:, : hq + hkv], a.cos()[:, None], a.sin()[:, None])
-    y = y.to(BF)
-    table = torch.arange(1, dtype=torch.int32)[None]
-    k = y[:, hq:].permute(1, 0, 2)[None].contiguous()
-    v = x[:, hq + hkv:].to(BF).permute(1, 0, 2)[None].contiguous()
-    return ref.attention(y[n - n_new:, :hq], k, v, table, [n], [0, n_new], causal)
+    a = torch.arange(x.shape[0], dtype=torch.float64)[:, None] * 10000.0 ** (-2 * j / d)
+    y, mag = ref.rotate(x[:, : hq + hkv], a.cos()[:, None], a.sin()[:, None])
+    # the table's cos and sin are rounded to fp32 (2^-24 of each product) on top of the kernel's own arithmetic
+    return y, ref.rotate_bound(y, mag) + ref.FP32_HALF * mag
 
 
 @pytest.mark.parametrize("heads,page", [(TINY, 16), (A4B, 64)])
 def test_a_serving_loop_of_plan_append_attention(heads, page):
+    """Every turn's q and every key and value of every request stand in the pages as its history says, and the
+    attention is that of these operands."""
     hq, hkv, d = heads
     width = (hq + 2 * hkv) * d
     g = torch.Generator().manual_seed(16)
@@ -552,20 +549,25 @@ def test_a_serving_loop_of_plan_append_attention(heads, page):
         rows = [max(0, n) for n in new]
         qkv = torch.randn(sum(rows), width, generator=g).to(BF)
         out, lse = s.turn(i32(new), qkv.cuda(), bool(causal))
-        o = out.cpu().double()
-        t0 = 0
+        q, k, v, table = s.q.cpu(), s.k.cpu(), s.v.cpu(), s.table.cpu()
+        cu = [0]
         for b, n in enumerate(new):
-            if n <= 0:
-                history[b] = history[b][: len(history[b]) + n]
+            cu.append(cu[-1] + max(0, n))
+            history[b] = torch.cat([history[b][: len(history[b]) + min(0, n)], qkv[cu[b]:cu[b + 1]]])
+            if not len(history[b]):
                 continue
-            history[b] = torch.cat([history[b], qkv[t0:t0 + n]])
-            w, _, tol, _ = contiguous(heads, history[b], n, causal)
-            # q and k go to bf16 through fp32 products: a value next to a tie may round the other way, one bf16
-            # step (2^-7) of a few of its D terms; a score moves by at most 2^-7 of its largest terms' sum
-            slack = 0.02 * w.abs().amax() + 0.02
-            assert ((o[t0:t0 + n] - w).abs() <= tol + slack).all()
-            assert (o[t0:t0 + n] - w).norm() <= 0.01 * w.norm()
-            t0 += n
+            y, tol = rotated(heads, history[b])
+            t = torch.arange(len(history[b]))
+            at, off = table[b, t // page].long(), t % page
+            assert ((k[at, :, off].double() - y[:, hq:]).abs() <= tol[:, hq:]).all()
+            assert torch.equal(v[at, :, off], history[b].view(-1, hq + 2 * hkv, d)[:, hq + hkv:])
+            if n > 0:
+                assert ((q[cu[b]:cu[b + 1]].double() - y[-n:, :hq]).abs() <= tol[-n:, :hq]).all()
+        lens = [len(h) for h in history]
+        assert s.kv.tolist() == lens
+        w, w_lse, tol, tol_l = ref.attention(q, k, v, table, lens, cu, bool(causal))
+        assert ((out.cpu().double() - w).abs() <= tol).all()
+        assert ((lse.cpu().double() - w_lse).abs() <= tol_l).all()
     state = s.state[0].tolist()
     held = sum(ref.pages_of(len(h), page) for h in history)
     assert state[1] == 64 - held and state[2:] == [0, 0]
