@@ -279,6 +279,87 @@ __device__ __forceinline__ void paged_list_none(const PagedAttnParams& p, const 
   if (g.tiles == 0 && p.cuts_by_tile && blockIdx.x == 0 && threadIdx.x == 0) p.cuts[0] = PagedCut{};
 }
 
+// A whole warp runs the code that issues tcgen05.mma or TMA copies, and one
+// elected lane's instructions take effect: descriptors, addresses and
+// coordinates then stay in uniform registers, where these instructions want
+// them (taken one lane at a time an instruction costs 65 to 110 cycles).
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t is;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(is));
+  return is;
+}
+
+__device__ __forceinline__ void tma_load_2d_lead(uint32_t lead, uint32_t smem_dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int x, int y, uint64_t policy) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;\n\t}" ::"r"(smem_dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "l"(policy), "r"(lead)
+      : "memory");
+}
+
+// Page ids of a request's row of the block table, 32 at a time, one per lane.
+struct PagedIds {
+  int first = -1, id = 0;
+  // fetch what the pieces of a block from page `page` on need
+  __device__ __forceinline__ void fetch(const PagedAttnParams& p, const int32_t* row, int page, int pieces) {
+    if (first >= 0 && page + pieces <= first + 32) return;
+    first = page;
+    const int mine = page + static_cast<int>(threadIdx.x & 31);
+    id = mine < p.width ? row[mine] : -1;
+  }
+  __device__ __forceinline__ int at(int page) const { return __shfl_sync(0xffffffffu, id, page - first); }
+};
+
+// The pages of a 64-key block: up to four pieces of `box` keys; their rows in
+// the pools' tensor maps for kv head h, and which keys exist.
+struct PagedBlock {
+  int row[4];
+  uint32_t good;               // pieces that lie in a page of the pool and below kv
+  uint64_t valid;              // keys that do
+};
+
+__device__ __forceinline__ PagedBlock paged_block(const PagedAttnParams& p, const PagedIds& ids, int kb, int kv, int h,
+                                                  int box, int piece_shift) {
+  PagedBlock b;
+  b.good = 0;
+  b.valid = 0;
+  const int first_page = (kb * PG_BK) >> p.page_shift;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >> piece_shift) break;
+    const int page = ids.at(first_page + i), key = kb * PG_BK + i * box;
+    b.row[i] = page * (p.Hkv << p.page_shift) + (h << p.page_shift) + (key & ((1 << p.page_shift) - 1));
+    if (page >= 0 && page < p.n_pages && key < kv) {
+      b.good |= 1u << i;
+      b.valid |= (box == 64 ? ~uint64_t(0) : ((uint64_t(1) << box) - 1)) << (i * box);
+    }
+  }
+  const int keys = kv - kb * PG_BK;
+  if (keys < PG_BK) b.valid &= keys > 0 ? (uint64_t(1) << keys) - 1 : 0;
+  return b;
+}
+
+// the DK column boxes of the block's pieces into a stage of [column box][64 keys][64 columns]
+template <int DK>
+__device__ __forceinline__ void paged_fetch(uint32_t lead, const PagedBlock& b, const CUtensorMap* map, uint32_t stage,
+                                            uint64_t* bar, int box, int piece_shift, uint64_t policy) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (i >> piece_shift) break;
+    if (!(b.good >> i & 1)) continue;
+#pragma unroll
+    for (int db = 0; db < DK; ++db)
+      tma_load_2d_lead(lead, stage + db * PG_BK * 128 + i * box * 128, map, bar, db * 64, b.row[i], policy);
+  }
+}
+
 // untiled copy of `bytes` (a multiple of 16; both addresses 16-byte aligned)
 __device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes, uint64_t* bar) {
   asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
@@ -436,13 +517,9 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
   if (warp == 0) {
     // ------------------------------- producer -------------------------------
     const int box = min(1 << p.page_shift, PG_BK);              // keys per TMA box
-    const int piece_shift = max(6 - p.page_shift, 0), pieces = 1 << piece_shift;  // pages (or part of one) per block
-    const int rows_per_page = p.Hkv << p.page_shift;
-    const int my_piece = lane & (pieces - 1), my_col = lane >> piece_shift;  // box of this lane: K columns, then V
-    const bool mine = my_col < 2 * C::DK;
-    const bool is_v = my_col >= C::DK;
-    const int db = is_v ? my_col - C::DK : my_col;
+    const int piece_shift = max(6 - p.page_shift, 0);           // 2^piece_shift pages (or part of one) per block
     const uint64_t pol = policy_evict_first();
+    const uint32_t lead = elect_one();
     int it = 0, seg = 0;
     uint32_t issued = 0, par = 0;
     PagedCut cut{};
@@ -450,31 +527,17 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       if (lane == 0) paged_list<TOK_ROWS>(p, g, w, seg, cut);
       const int32_t* tab = p.table + w.b * p.table_stride;
       const int live = min((w.r.n << p.g_shift) - w.tile * TOK_ROWS, TOK_ROWS);
-      int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
+      PagedIds ids;
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         const int s = it % C::STAGES;
-        const int first_page = (kb * PG_BK) >> p.page_shift;
-        if (ids0 < 0 || first_page + pieces > ids0 + 32) {
-          ids0 = first_page;
-          ids = ids0 + lane < p.width ? tab[ids0 + lane] : -1;
-        }
+        ids.fetch(p, tab, (kb * PG_BK) >> p.page_shift, 1 << piece_shift);
+        const PagedBlock blk = paged_block(p, ids, kb, w.r.kv, w.h, box, piece_shift);
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err) && !*abort_flag);
         if (!ok) break;
-        const int page = __shfl_sync(0xffffffffu, ids, first_page + my_piece - ids0);
-        const int key = kb * PG_BK + my_piece * box;
-        const bool good = page >= 0 && page < p.n_pages && key < w.r.kv;
-        // lanes 0 .. pieces-1 hold one piece each
-        const uint32_t pmask = __ballot_sync(0xffffffffu, good && lane < pieces);
-        uint8_t* stage = smem + s * 2 * C::KV_BYTES;
-        if (lane == 0) {
-          uint64_t valid = 0;
-          for (int i = 0; i < pieces; ++i)
-            if (pmask >> i & 1) valid |= (box == 64 ? ~uint64_t(0) : ((uint64_t(1) << box) - 1)) << (i * box);
-          const int keys = w.r.kv - kb * PG_BK;
-          if (keys < PG_BK) valid &= keys > 0 ? (uint64_t(1) << keys) - 1 : 0;
-          const bool first = kb == w.kb0;
+        const bool first = kb == w.kb0;
+        if (lead) {
           TokDesc d;
-          d.valid = valid;
+          d.valid = blk.valid;
           d.flags = (first ? TOK_FIRST : 0) | (kb + 1 == w.kb1 ? TOK_LAST : 0) | (w.whole() ? TOK_WHOLE : 0) |
                     (seg > 0 ? TOK_SLOT1 : 0);
           d.qbuf = seg % C::Q_BUFS;
@@ -485,15 +548,12 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
           d.row0 = w.tile * TOK_ROWS;
           d.key0 = kb * PG_BK;
           desc[s] = d;
-          mbar_arrive_expect_tx(&full[s], __popc(pmask) * box * 128 * 2 * C::DK + (first ? live * D * 2 : 0));
+          mbar_arrive_expect_tx(&full[s], __popc(blk.good) * box * 128 * 2 * C::DK + (first ? live * D * 2 : 0));
         }
         __syncwarp();
-        if (mine && good) {
-          const int off = key & ((1 << p.page_shift) - 1);
-          tma_load_2d(stage + (is_v ? C::KV_BYTES : 0) + db * PG_BK * 128 + my_piece * box * 128,
-                      is_v ? &p.v_map : &p.k_map, &full[s], db * 64,
-                      page * rows_per_page + (w.h << p.page_shift) + off, pol);
-        }
+        const uint32_t stage = smem_u32(smem) + s * 2 * C::KV_BYTES;
+        paged_fetch<C::DK>(lead, blk, &p.k_map, stage, &full[s], box, piece_shift, pol);
+        paged_fetch<C::DK>(lead, blk, &p.v_map, stage + C::KV_BYTES, &full[s], box, piece_shift, pol);
         if (kb == w.kb0 && lane < live) {
           const int r = w.tile * TOK_ROWS + lane;
           bulk_load(s_q + (seg % C::Q_BUFS) * C::Q_BYTES + lane * D * 2,

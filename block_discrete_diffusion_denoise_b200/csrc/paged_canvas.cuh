@@ -54,20 +54,6 @@ struct CanvasParams {
   CUtensorMap q_map;           // 4-D (D, G, Hkv, rows) over q; box (64, G, 1, 128 / G)
 };
 
-// The whole MMA warp runs the issuing code, and one elected lane's
-// instructions take effect: descriptors and addresses then stay in uniform
-// registers, where tcgen05.mma wants them (a lane-0 branch took 65 cycles per
-// instruction to move them there, the products themselves 48 to 88).
-__device__ __forceinline__ uint32_t elect_one() {
-  uint32_t is;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "elect.sync _|p, 0xffffffff;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(is));
-  return is;
-}
-
 // Matrix descriptors of one operand that differ in their start address only:
 // the low word carries it (16-byte units), the high word is the layout.
 struct UmmaOperand {
@@ -202,9 +188,8 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     uint64_t* empty = is_k ? k_empty : v_empty;
     uint8_t* ring = smem + (is_k ? C::K_OFF : C::V_OFF);
     const int box = min(1 << p.page_shift, PG_BK);              // keys per TMA box
-    const int piece_shift = max(6 - p.page_shift, 0), pieces = 1 << piece_shift;  // pages (or part of one) per block
-    const int rows_per_page = p.Hkv << p.page_shift;
-    const int my_piece = lane & (pieces - 1), db = lane >> piece_shift;           // box of this lane
+    const int piece_shift = max(6 - p.page_shift, 0);           // 2^piece_shift pages (or part of one) per block
+    const uint32_t lead = elect_one();
     const uint64_t pol = policy_evict_last();                   // the request's other row tiles read the block again
     int it = 0, seg = 0;
     uint32_t issued = 0, par = 0;
@@ -212,37 +197,21 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
     for (PagedWalk<CV_ROWS> w(g); ok && w.more(); w.next(p), ++seg) {
       if (!is_k && lane == 0) paged_list<CV_ROWS>(p, g, w, seg, cut);
       const int32_t* tab = p.table + w.b * p.table_stride;
-      int ids0 = -1, ids = 0;                                   // page ids [ids0, ids0 + 32) of the request, one per lane
+      PagedIds ids;
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         const int s = it % C::STAGES;
-        const int first_page = (kb * PG_BK) >> p.page_shift;
-        if (ids0 < 0 || first_page + pieces > ids0 + 32) {
-          ids0 = first_page;
-          ids = ids0 + lane < p.width ? tab[ids0 + lane] : -1;
-        }
-        const int page = __shfl_sync(0xffffffffu, ids, first_page + my_piece - ids0);
-        const int key = kb * PG_BK + my_piece * box;
-        const bool good = page >= 0 && page < p.n_pages && key < w.r.kv;
-        const uint32_t pmask = __ballot_sync(0xffffffffu, good && lane < pieces);
+        ids.fetch(p, tab, (kb * PG_BK) >> p.page_shift, 1 << piece_shift);
+        const PagedBlock blk = paged_block(p, ids, kb, w.r.kv, w.h, box, piece_shift);
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err) && !*abort_flag);
         if (!ok) break;
-        if (lane == 0) {
-          if (is_k) {
-            uint64_t valid = 0;
-            for (int i = 0; i < pieces; ++i)
-              if (pmask >> i & 1) valid |= (box == 64 ? ~uint64_t(0) : ((uint64_t(1) << box) - 1)) << (i * box);
-            const int keys = w.r.kv - kb * PG_BK;
-            if (keys < PG_BK) valid &= keys > 0 ? (uint64_t(1) << keys) - 1 : 0;
-            // the slot's last reader has read it: this K slot came free STAGES units behind it, and the softmax of a
-            // tile is never more than two units behind its scores
-            key_mask[it % CV_MASKS] = valid;
-          }
-          mbar_arrive_expect_tx(&full[s], __popc(pmask) * box * 128 * C::DK);
+        if (lead) {
+          // the mask's slot has been read by all: this K slot came free STAGES units behind its last user, and the
+          // softmax of a tile is never more than two units behind its scores
+          if (is_k) key_mask[it % CV_MASKS] = blk.valid;
+          mbar_arrive_expect_tx(&full[s], __popc(blk.good) * box * 128 * C::DK);
         }
         __syncwarp();
-        if (db < C::DK && good)
-          tma_load_2d(ring + s * C::KV_BYTES + db * PG_BK * 128 + my_piece * box * 128, map, &full[s], db * 64,
-                      page * rows_per_page + (w.h << p.page_shift) + (key & ((1 << p.page_shift) - 1)), pol);
+        paged_fetch<C::DK>(lead, blk, map, smem_u32(ring) + s * C::KV_BYTES, &full[s], box, piece_shift, pol);
         issued |= 1u << s;
         par = (par & ~(1u << s)) | (((it / C::STAGES) & 1) << s);
       }
