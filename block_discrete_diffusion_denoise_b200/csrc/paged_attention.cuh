@@ -407,25 +407,29 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // Bound by HBM: 4 D bytes per key and kv head against 2 x 16 x 2 D operations,
 // of which a token's G rows are useful.  So the products run on mma.sync
 // (64 x 16 x 2 D x 2 per block, under a tenth of the block's time on the
-// memory), and everything else serves the stream of pages: one producer warp
-// keeps TOK_STAGES blocks of K and V in flight, each landing swizzled by TMA
+// memory), and everything else serves the stream of pages: two producer
+// warps keep STAGES blocks of K and V in flight, each landing swizzled by TMA
 // so that ldmatrix reads it without bank conflicts; four warps take 16 of its
 // 64 keys each, with running maxima, sums and rows of their own (no barrier
-// between them inside a tile), joined through shared memory at a tile's end.
+// between them inside a tile); at a tile's end they leave these in shared
+// memory and go on, and a warp of its own joins them.
 // One token for 64 requests of 256..8190 keys, 16/8 heads of 176: 233 us with
 // the merge, 6.6 TB/s (1.0 of the copy peak); one request of 2048 keys: 9.1 us,
 // of which the two blocks of a CTA are one.
 // ----------------------------------------------------------------------------
 constexpr int TOK_ROWS = 16;
 constexpr int TOK_WARPS = 4;                       // consumer warps
-constexpr int TOK_THREADS = 32 * (1 + TOK_WARPS);
+constexpr int TOK_FIRST_CONSUMER = 2;              // warps 0 K, Q and descriptors, 1 V, 2..5 consumers, 6 join
+constexpr int TOK_JOIN_WARP = TOK_FIRST_CONSUMER + TOK_WARPS;
+constexpr int TOK_THREADS = 32 * (TOK_JOIN_WARP + 1);
 
 template <int D>
 struct TokCfg {
   static constexpr int DK = (D + 63) / 64;
   static constexpr int KV_BYTES = DK * PG_BK * 128;             // K or V of a block
   static constexpr int STAGES = D == 64 ? 6 : D == 128 ? 4 : 3;
-  static constexpr int Q_BYTES = TOK_ROWS * D * 2;
+  static constexpr int Q_LD = D * 2 + 16;                       // bytes of a query row: eight rows in different banks
+  static constexpr int Q_BYTES = TOK_ROWS * Q_LD;
   static constexpr int Q_BUFS = STAGES + 1;                     // a tile's rows arrive with its first block
   static constexpr int O_LD = D + 4;
   static constexpr int O_BYTES = TOK_WARPS * TOK_ROWS * O_LD * 4;
@@ -435,13 +439,13 @@ struct TokCfg {
   static constexpr int SMEM = 1024 + TAIL_OFF + 1536;
 };
 
-enum TokFlags : int { TOK_FIRST = 1, TOK_LAST = 2, TOK_EXIT = 4, TOK_WHOLE = 8, TOK_SLOT1 = 16 };
+enum TokFlags : int { TOK_FIRST = 1, TOK_LAST = 2, TOK_EXIT = 4 };
 
 // what the consumers need to know of a stage
 struct TokDesc {
   uint64_t valid;              // keys of the block in pages of the pool, below kv
   int flags, qbuf;
-  int t0, n, kv, h;
+  int n, kv;
   int row0;                    // first packed row of the tile
   int key0;                    // first key of the block
 };
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
   uint64_t* full = reinterpret_cast<uint64_t*>(tail);
   uint64_t* empty = full + C::STAGES;
   uint64_t* o_full = empty + C::STAGES;                         // all four warps' rows of a tile written
-  uint64_t* o_free = o_full + 1;                                // ... and read again
+  uint64_t* o_free = o_full + 1;                                // ... and joined
   TokDesc* desc = reinterpret_cast<TokDesc*>(tail + 256);       // [STAGES]
   float2* s_ml = reinterpret_cast<float2*>(tail + 768);         // [warp][16]
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tail + 1280);
@@ -501,11 +505,11 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     tma_prefetch_desc(&p.k_map);
     tma_prefetch_desc(&p.v_map);
     for (int s = 0; s < C::STAGES; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);                  // both producers
       mbar_init(&empty[s], TOK_WARPS);
     }
     mbar_init(o_full, TOK_WARPS);
-    mbar_init(o_free, TOK_WARPS);
+    mbar_init(o_free, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -514,8 +518,10 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
   paged_list_none(p, g);
   bool ok = true;
 
-  if (warp == 0) {
-    // ------------------------------- producer -------------------------------
+  if (warp < TOK_FIRST_CONSUMER) {
+    // ------------------ producers: warp 0 K, Q and descriptors, warp 1 V ------------------
+    const bool is_k = warp == 0;
+    const CUtensorMap* map = is_k ? &p.k_map : &p.v_map;
     const int box = min(1 << p.page_shift, PG_BK);              // keys per TMA box
     const int piece_shift = max(6 - p.page_shift, 0);           // 2^piece_shift pages (or part of one) per block
     const uint64_t pol = policy_evict_first();
@@ -524,7 +530,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     uint32_t issued = 0, par = 0;
     PagedCut cut{};
     for (PagedWalk<TOK_ROWS> w(g); ok && w.more(); w.next(p), ++seg) {
-      if (lane == 0) paged_list<TOK_ROWS>(p, g, w, seg, cut);
+      if (!is_k && lane == 0) paged_list<TOK_ROWS>(p, g, w, seg, cut);
       const int32_t* tab = p.table + w.b * p.table_stride;
       const int live = min((w.r.n << p.g_shift) - w.tile * TOK_ROWS, TOK_ROWS);
       PagedIds ids;
@@ -534,29 +540,27 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
         const PagedBlock blk = paged_block(p, ids, kb, w.r.kv, w.h, box, piece_shift);
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err) && !*abort_flag);
         if (!ok) break;
-        const bool first = kb == w.kb0;
+        const bool with_q = is_k && kb == w.kb0;
         if (lead) {
-          TokDesc d;
-          d.valid = blk.valid;
-          d.flags = (first ? TOK_FIRST : 0) | (kb + 1 == w.kb1 ? TOK_LAST : 0) | (w.whole() ? TOK_WHOLE : 0) |
-                    (seg > 0 ? TOK_SLOT1 : 0);
-          d.qbuf = seg % C::Q_BUFS;
-          d.t0 = w.r.t0;
-          d.n = w.r.n;
-          d.kv = w.r.kv;
-          d.h = w.h;
-          d.row0 = w.tile * TOK_ROWS;
-          d.key0 = kb * PG_BK;
-          desc[s] = d;
-          mbar_arrive_expect_tx(&full[s], __popc(blk.good) * box * 128 * 2 * C::DK + (first ? live * D * 2 : 0));
+          if (is_k) {
+            TokDesc d;
+            d.valid = blk.valid;
+            d.flags = (kb == w.kb0 ? TOK_FIRST : 0) | (kb + 1 == w.kb1 ? TOK_LAST : 0);
+            d.qbuf = seg % C::Q_BUFS;
+            d.n = w.r.n;
+            d.kv = w.r.kv;
+            d.row0 = w.tile * TOK_ROWS;
+            d.key0 = kb * PG_BK;
+            desc[s] = d;
+          }
+          mbar_arrive_expect_tx(&full[s], __popc(blk.good) * box * 128 * C::DK + (with_q ? live * D * 2 : 0));
         }
         __syncwarp();
-        const uint32_t stage = smem_u32(smem) + s * 2 * C::KV_BYTES;
-        paged_fetch<C::DK>(lead, blk, &p.k_map, stage, &full[s], box, piece_shift, pol);
-        paged_fetch<C::DK>(lead, blk, &p.v_map, stage + C::KV_BYTES, &full[s], box, piece_shift, pol);
-        if (kb == w.kb0 && lane < live) {
+        paged_fetch<C::DK>(lead, blk, map, smem_u32(smem) + s * 2 * C::KV_BYTES + (is_k ? 0 : C::KV_BYTES), &full[s],
+                           box, piece_shift, pol);
+        if (with_q && lane < live) {
           const int r = w.tile * TOK_ROWS + lane;
-          bulk_load(s_q + (seg % C::Q_BUFS) * C::Q_BYTES + lane * D * 2,
+          bulk_load(s_q + (seg % C::Q_BUFS) * C::Q_BYTES + lane * C::Q_LD,
                     p.q + (w.r.t0 + (r >> p.g_shift)) * p.q_stride +
                         ((w.h << p.g_shift) + (r & ((1 << p.g_shift) - 1))) * D,
                     D * 2, &full[s]);
@@ -566,10 +570,10 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       }
     }
     if (lane == 0) {
-      if (!p.cuts_by_tile) p.cuts[blockIdx.x] = cut;
+      if (!is_k && !p.cuts_by_tile) p.cuts[blockIdx.x] = cut;
       const int s = it % C::STAGES;
       if (ok && mbar_wait(&empty[s], ((it / C::STAGES) & 1) ^ 1, p.err)) {
-        desc[s].flags = TOK_EXIT;
+        if (is_k) desc[s].flags = TOK_EXIT;
         mbar_arrive(&full[s]);
       } else {
         *abort_flag = 1;
@@ -578,9 +582,9 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
           if (issued >> x & 1) mbar_wait(&full[x], par >> x & 1, p.err);
       }
     }
-  } else {
+  } else if (warp < TOK_JOIN_WARP) {
     // ------------------------------- consumers ------------------------------
-    const int w = warp - 1, gr = lane >> 2, c = lane & 3, mi = lane >> 3, mr = lane & 7;
+    const int w = warp - TOK_FIRST_CONSUMER, gr = lane >> 2, c = lane & 3, mi = lane >> 3, mr = lane & 7;
     uint32_t qf[D / 16][4];
     float o[D / 8][4];
     float m[2], l[2];
@@ -597,7 +601,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
         const uint32_t q_at = smem_u32(s_q + d.qbuf * C::Q_BYTES);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
-          ldmatrix_x4(qf[kk], q_at + ((mi & 1) * 8 + mr) * (D * 2) + kk * 32 + (mi >> 1) * 16);
+          ldmatrix_x4(qf[kk], q_at + ((mi & 1) * 8 + mr) * C::Q_LD + kk * 32 + (mi >> 1) * 16);
 #pragma unroll
         for (int t = 0; t < D / 8; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
 #pragma unroll
@@ -679,7 +683,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       if (lane == 0) mbar_arrive(&empty[s]);
       if (!(d.flags & TOK_LAST)) continue;
 
-      // -------- the tile's end: the four warps' rows joined in order --------
+      // -------- the tile's end: this warp's rows, once those of the tile before are joined --------
       const int live = min((d.n << p.g_shift) - d.row0, TOK_ROWS);
       if (seg > 0) {
         ok = __all_sync(0xffffffffu, mbar_wait(o_free, (seg - 1) & 1, p.err) && !*abort_flag);
@@ -699,10 +703,20 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(o_full);
+      ++seg;
+    }
+    if (!ok) *abort_flag = 1;
+  } else {
+    // ---------------- join: the four warps' rows of a tile, in order ----------------
+    int seg = 0;
+    for (PagedWalk<TOK_ROWS> w(g); w.more(); w.next(p), ++seg) {
       ok = __all_sync(0xffffffffu, mbar_wait(o_full, seg & 1, p.err) && !*abort_flag);
       if (!ok) break;
-      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (d.flags & TOK_SLOT1 ? 1 : 0);
-      for (int i = threadIdx.x - 32; i < live * (D / 4); i += 32 * TOK_WARPS) {
+      const int row0 = w.tile * TOK_ROWS, live = min((w.r.n << p.g_shift) - row0, TOK_ROWS);
+      const bool whole = w.whole();
+      const int64_t slot = static_cast<int64_t>(blockIdx.x) * 2 + (seg > 0);
+#pragma unroll 2
+      for (int i = lane; i < live * (D / 4); i += 32) {
         const int r = i / (D / 4), c4 = i % (D / 4) * 4;
         float M = -INFINITY;
 #pragma unroll
@@ -721,9 +735,9 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
           a.z += e * v.z;
           a.w += e * v.w;
         }
-        if (d.flags & TOK_WHOLE) {
+        if (whole) {
           const float inv = L == 0.f ? 0.f : 1.f / L;
-          const int64_t row = paged_out_row(p, d.t0, d.row0 + r, d.h);
+          const int64_t row = paged_out_row(p, w.r.t0, row0 + r, w.h);
           *reinterpret_cast<uint2*>(p.o + row * D + c4) =
               make_uint2(cvt_bf16x2(a.x * inv, a.y * inv), cvt_bf16x2(a.z * inv, a.w * inv));
           if (p.lse && c4 == 0) p.lse[row] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.69314718055994531f;
@@ -734,7 +748,6 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(o_free);
-      ++seg;
     }
     if (!ok) *abort_flag = 1;
   }
