@@ -50,7 +50,8 @@ struct PagedAttnParams {
 };
 
 struct PagedRequest {
-  int t0, n, kv, tiles;        // first row, rows, keys, row tiles
+  int t0, n, kv, tiles;        // first row, rows, keys (of those the table holds), row tiles
+  int before;                  // keys before the first row's own; less than -1 where the first rows see none
 };
 
 template <int ROWS>
@@ -58,7 +59,9 @@ __device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams& p, 
   PagedRequest r;
   r.t0 = min(max(p.cu_rows[b], 0), p.rows);
   r.n = max(min(p.cu_rows[b + 1], p.rows) - r.t0, 0);
-  r.kv = min(max(p.kv_lens[b], 0), p.width << p.page_shift);
+  const int len = max(p.kv_lens[b], 0);
+  r.kv = min(len, p.width << p.page_shift);
+  r.before = len - r.n;
   r.tiles = ((r.n << p.g_shift) + ROWS - 1) / ROWS;
   return r;
 }
@@ -68,7 +71,7 @@ template <int ROWS>
 __device__ __forceinline__ int paged_blocks(const PagedAttnParams& p, const PagedRequest& r, int t) {
   int keys = r.kv;
   if (p.causal && t + 1 < r.tiles)
-    keys = min(keys, r.kv - r.n + (((t + 1) * ROWS - 1) >> p.g_shift) + 1);
+    keys = min(keys, r.before + (((t + 1) * ROWS - 1) >> p.g_shift) + 1);
   return keys > 0 ? (keys - 1) / PG_BK + 1 : 1;   // a tile without keys still writes its rows
 }
 
@@ -439,13 +442,13 @@ struct TokCfg {
   static constexpr int SMEM = 1024 + TAIL_OFF + 1536;
 };
 
-enum TokFlags : int { TOK_FIRST = 1, TOK_LAST = 2, TOK_EXIT = 4 };
+enum TokFlags : int { TOK_FIRST = 1, TOK_LAST = 2, TOK_EXIT = 4, TOK_QBUF_SHIFT = 8 };
 
 // what the consumers need to know of a stage
 struct TokDesc {
   uint64_t valid;              // keys of the block in pages of the pool, below kv
-  int flags, qbuf;
-  int n, kv;
+  int flags;                   // TokFlags | buffer of the tile's queries << TOK_QBUF_SHIFT
+  int n, kv, before;           // PagedRequest
   int row0;                    // first packed row of the tile
   int key0;                    // first key of the block
 };
@@ -545,10 +548,11 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
           if (is_k) {
             TokDesc d;
             d.valid = blk.valid;
-            d.flags = (kb == w.kb0 ? TOK_FIRST : 0) | (kb + 1 == w.kb1 ? TOK_LAST : 0);
-            d.qbuf = seg % C::Q_BUFS;
+            d.flags = (kb == w.kb0 ? TOK_FIRST : 0) | (kb + 1 == w.kb1 ? TOK_LAST : 0) |
+                      (seg % C::Q_BUFS) << TOK_QBUF_SHIFT;
             d.n = w.r.n;
             d.kv = w.r.kv;
+            d.before = w.r.before;
             d.row0 = w.tile * TOK_ROWS;
             d.key0 = kb * PG_BK;
             desc[s] = d;
@@ -598,7 +602,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
       if (d.flags & TOK_EXIT) break;
       const uint32_t k_at = smem_u32(smem + s * 2 * C::KV_BYTES), v_at = k_at + C::KV_BYTES;
       if (d.flags & TOK_FIRST) {
-        const uint32_t q_at = smem_u32(s_q + d.qbuf * C::Q_BYTES);
+        const uint32_t q_at = smem_u32(s_q + (d.flags >> TOK_QBUF_SHIFT) * C::Q_BYTES);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk)
           ldmatrix_x4(qf[kk], q_at + ((mi & 1) * 8 + mr) * C::Q_LD + kk * 32 + (mi >> 1) * 16);
@@ -608,7 +612,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
         for (int x = 0; x < 2; ++x) {
           m[x] = -INFINITY;
           l[x] = 0.f;
-          lim[x] = p.causal ? min(d.kv, d.kv - d.n + ((d.row0 + gr + 8 * x) >> p.g_shift) + 1) : d.kv;
+          lim[x] = p.causal ? min(d.kv, d.before + ((d.row0 + gr + 8 * x) >> p.g_shift) + 1) : d.kv;
         }
       }
       // S = Q K^T for this warp's 16 keys: two 16 x 8 tiles

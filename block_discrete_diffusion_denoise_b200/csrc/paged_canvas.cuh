@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
       const int r = row0 + wg * CV_TILE + rloc;      // packed row of the request
       const bool live = r < (w.r.n << p.g_shift);
       // keys [0, lim) are this row's
-      const int lim = !live ? 0 : p.causal ? min(w.r.kv, w.r.kv - w.r.n + (r >> p.g_shift) + 1) : w.r.kv;
+      const int lim = !live ? 0 : p.causal ? min(w.r.kv, w.r.before + (r >> p.g_shift) + 1) : w.r.kv;
       const int lim_all = __reduce_min_sync(0xffffffffu, live ? lim : INT32_MAX);
       float mref = -INFINITY, lsum = 0.f;
       for (int u = 0; u < units; ++u, ++j, ++n_s) {

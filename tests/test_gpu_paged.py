@@ -313,6 +313,17 @@ def test_attention_clamps_lengths_to_the_table(rows):
     assert torch.equal(o2, out)
 
 
+@pytest.mark.parametrize("rows", [1, 3, 64])
+def test_causal_rows_keep_their_places_beyond_the_table(rows):
+    """a row's last key goes by the request's own length, where the table holds fewer pages too"""
+    g = torch.Generator().manual_seed(22)
+    q, k, v, table, cu = paged_cache(g, SMALL, 16, [160, 96], [rows] * 2)
+    k, v = torch.nan_to_num(k, nan=1.0), torch.nan_to_num(v, nan=2.0)
+    table = table.clamp(0, k.shape[0] - 1)
+    check_attention(q, k, v, table, [table.shape[1] * 16 + 30, 96 + 2], cu, True, max_rows=rows)
+    check_attention(q, k, v, table, [table.shape[1] * 16 + 3, 90], cu, True, max_rows=rows)
+
+
 @pytest.mark.parametrize("rows", [1, 40])
 def test_attention_takes_strided_queries_and_tables(rows):
     hq, hkv, d = A4B
