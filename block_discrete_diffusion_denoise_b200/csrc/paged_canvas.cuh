@@ -143,7 +143,6 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   static_assert((2 + 4 * C::STAGES + 20) * 8 <= 512 && CV_MASKS * 8 <= 448, "tail layout");
   static_assert(CV_MASKS >= C::STAGES + 4, "a mask is read before its slot comes round");
 
-  pdl_launch_dependents();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&p.k_map);
@@ -171,6 +170,8 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   if (warp == CV_MMA_WARP) {
     tmem_alloc(tmem_holder, C::TMEM_COLS);
     tmem_relinquish();
+    // Not before TMEM is this CTA's: a kernel that took it first and waits for this one would never get on.
+    pdl_launch_dependents();
   }
   tc_fence_before();
   pdl_wait();
