@@ -152,6 +152,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int 
     warp_sum[warp] = upto;
     warp_tiles[warp] = tiles_upto;
   }
+  if (threadIdx.x == 0) found.left = 0;   // nobody finds it if lengths change under the call
   __syncthreads();
   long long total = 0, before = 0;
   int tiles_all = 0, tiles_before = 0;
@@ -181,7 +182,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int 
       for (;; ++b) {
         r = paged_request<ROWS>(p, b);
         const long long u = paged_units<ROWS>(p, r);
-        if (lo < at + u) break;
+        if (lo < at + u || b + 1 == b1) break;
         at += u;
         tiles_at += r.tiles * p.Hkv;
       }
@@ -193,7 +194,7 @@ __device__ __forceinline__ PagedRange paged_range(const PagedAttnParams& p, int 
     if (!p.causal) {
       g.tile = static_cast<int>(div64(x, static_cast<int64_t>(g.nb) * p.Hkv, x));
     } else {
-      while (x >= static_cast<int64_t>(g.nb) * p.Hkv) {
+      while (x >= static_cast<int64_t>(g.nb) * p.Hkv && g.tile + 1 < r.tiles) {
         x -= static_cast<int64_t>(g.nb) * p.Hkv;
         g.nb = paged_blocks<ROWS>(p, r, ++g.tile);
       }
