@@ -8,6 +8,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <new>
 #include <string>
 #include <vector>
 
@@ -501,6 +502,12 @@ dg_status ragged_adopt(dg_ctx* c, const std::vector<int32_t>& rows) {
   c->rg_cur ^= 1;
   for (int b = 0; b < c->B; ++b) c->lens[b] += rows[b];
   return DG_OK;
+}
+
+// host memory ran out inside an entry point: no exception leaves it
+dg_status host_oom(dg_ctx* c) {
+  c->last_error = "host memory";   // short enough to need none
+  return DG_ERR_OOM;
 }
 
 // pages that the batch needs with `more` positions behind each of `lens`
@@ -1302,6 +1309,12 @@ dg_status dg_create(const dg_config* cfg, const dg_weights* w, void* cuda_stream
     discard(c);
     return st;
   }
+  try {
+    c->lens.reserve(g.max_batch);
+  } catch (const std::bad_alloc&) {
+    free_all(c);
+    return reject(DG_ERR_OOM, "host memory");
+  }
   *out = c;
   return DG_OK;
 }
@@ -1322,7 +1335,7 @@ dg_status dg_prefill(dg_ctx* c, const int32_t* tokens, int32_t B, int32_t P) {
   c->B = B;
   c->P = 0;
   c->ragged = false;
-  c->lens.assign(B, P);
+  c->lens.assign(B, P);        // within what dg_create reserved
   c->prefilled = false;
   c->sc_valid = false;  // a new canvas starts without a self-conditioning signal
   const int chunk = std::max(1, c->R / B);
@@ -1336,7 +1349,7 @@ dg_status dg_prefill(dg_ctx* c, const int32_t* tokens, int32_t B, int32_t P) {
   return DG_OK;
 }
 
-dg_status dg_prefill_ragged(dg_ctx* c, const int32_t* tokens, int32_t B, const int32_t* lens) {
+dg_status dg_prefill_ragged(dg_ctx* c, const int32_t* tokens, int32_t B, const int32_t* lens) try {
   if (!c) return DG_ERR_INVALID_ARG;
   if (!tokens || !lens || B <= 0) return fail(c, DG_ERR_INVALID_ARG, "prefill_ragged: bad arguments");
   if (B > c->cfg.max_batch) return fail(c, DG_ERR_CAPACITY, "prefill_ragged: batch %d beyond capacity", B);
@@ -1413,6 +1426,8 @@ dg_status dg_prefill_ragged(dg_ctx* c, const int32_t* tokens, int32_t B, const i
   if (st != DG_OK) return st;
   c->prefilled = true;
   return DG_OK;
+} catch (const std::bad_alloc&) {
+  return host_oom(c);
 }
 
 dg_status dg_denoise_step(dg_ctx* c, const int32_t* canvas_in, int32_t step, uint64_t seed, float tau,
@@ -1471,7 +1486,7 @@ dg_status dg_denoise_step_host(dg_ctx* c, const int32_t* canvas_in_host, int32_t
   return dg_sync(c);
 }
 
-dg_status dg_commit_block(dg_ctx* c, const int32_t* block) {
+dg_status dg_commit_block(dg_ctx* c, const int32_t* block) try {
   if (!c) return DG_ERR_INVALID_ARG;
   if (!block) return fail(c, DG_ERR_INVALID_ARG, "commit: null block");
   if (!c->prefilled) return fail(c, DG_ERR_STATE, "commit before prefill");
@@ -1492,6 +1507,8 @@ dg_status dg_commit_block(dg_ctx* c, const int32_t* block) {
   c->P += c->cfg.canvas;
   c->sc_valid = false;  // the next block starts without a self-conditioning signal
   return DG_OK;
+} catch (const std::bad_alloc&) {
+  return host_oom(c);
 }
 
 dg_status dg_sync(dg_ctx* c) {
