@@ -511,6 +511,7 @@ def lmhead_argmax_static(z, embed, temperature, argmax=None, lse=None, conf=None
 # torch offers bound to module names; what is wrong with a bad one is found
 # again, condition by condition, in order to say it.
 _BF16 = _I32 = _F32 = _current_device = _raw_stream = None
+_I32_MAX = 2 ** 31 - 1
 
 
 def _bind_torch():
@@ -606,8 +607,9 @@ def paged_plan(cached_lens, new_rows, block_table, free_pages, free_state, page_
                 and free_state.is_contiguous() and cu_rows.is_contiguous() and kv_lens.is_contiguous()
                 and positions.is_contiguous() and slots.is_contiguous() and free_state_out.is_contiguous())
         stride = W if block_table.is_contiguous() else block_table.stride(0)
-        good = good and (stride == W or block_table.stride(1) == 1 or W == 1)
-    except (AttributeError, ValueError):
+        good = (good and (stride == W or block_table.stride(1) == 1 or W == 1)
+                and cap <= _I32_MAX and free_pages.numel() <= _I32_MAX and 0 <= page_size <= _I32_MAX)
+    except (AttributeError, TypeError, ValueError):
         good = False
     if not good:
         _paged_check_table(block_table, None)
@@ -619,7 +621,7 @@ def paged_plan(cached_lens, new_rows, block_table, free_pages, free_state, page_
                            (free_state, 2, "free_state"), (cu_rows, B + 1, "cu_rows"), (kv_lens, B, "kv_lens"),
                            (positions, slots.numel(), "positions"), (free_state_out, 4, "free_state_out")):
             _paged_check_ints(t, n, what, idx)
-        _invalid("arguments")
+        _invalid("page_size, or the number of free_pages or slots: expected a number of 32 bits")
     _paged_call(_lib.dg_paged_plan, idx, cached_lens.data_ptr(), new_rows.data_ptr(), B, block_table.data_ptr(), W,
                 stride if B > 1 else W, free_pages.data_ptr(), free_pages.numel(), free_state.data_ptr(), page_size,
                 cu_rows.data_ptr(), kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), cap,
@@ -746,22 +748,27 @@ def paged_attention(q, k_pages, v_pages, block_table, kv_lens, cu_rows, out, lse
     if hkv == 0 or hq % hkv:
         raise DGError(DG_ERR_UNSUPPORTED, f"{hq} query heads on {hkv} kv heads")
     # its workspace's size goes by the device and these numbers alone, and all bounds of over 16 rows are alike
-    key = (idx, d, hq // hkv, min(max_rows if 0 < max_rows < rows else rows, 17))
-    need = _paged_workspace_bytes.get(key, 0)
-    if need:
-        # from torch's allocator: calls on other streams and in other graphs get memory of their own
-        ws = q.new_empty(need // 2)
-    args = (q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
+    try:
+        bound = max_rows if 0 < max_rows < rows else rows
+        key = (idx, d, hq // hkv, min(bound, 17))
+        need = _paged_workspace_bytes.get(key, 0)
+        if need:
+            # from torch's allocator: calls on other streams and in other graphs get memory of their own
+            ws = q.new_empty(need // 2)
+        args = _PAGED_ATTENTION_ARGS.pack(
+            q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), block_table.data_ptr(), kv_lens.data_ptr(),
             cu_rows.data_ptr(), out.data_ptr(), lse_at, ws.data_ptr() if need else 0, need,
             q_stride if rows > 1 else hq * d, stride if B > 1 else W, rows, B, hq, hkv, d, n_pages, page, W,
-            1 if causal else 0, max_rows, d ** -0.5 if scale is None else scale)
+            1 if causal else 0, bound, d ** -0.5 if scale is None else scale)
+    except (TypeError, OverflowError, struct.error):
+        _invalid("max_rows, scale: expected a number of 32 bits, and one that fits float32")
     if need:
-        _paged_call(_lib.dg_paged_attention, idx, _PAGED_ATTENTION_ARGS.pack(*args))
+        _paged_call(_lib.dg_paged_attention, idx, args)
         return
     n = ctypes.c_int64()
     import torch
     with torch.cuda.device(idx):
-        st = _lib.dg_paged_attention_workspace(_PAGED_ATTENTION_ARGS.pack(*args), ctypes.byref(n))
+        st = _lib.dg_paged_attention_workspace(args, ctypes.byref(n))
     if st != DG_OK:
         raise DGError(st, "dg_paged_attention refused (shape, alignment or capacity; see include/dg.h)")
     _paged_workspace_bytes[key] = n.value

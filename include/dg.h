@@ -49,7 +49,7 @@ typedef struct dg_ctx dg_ctx;
 typedef enum dg_status {
   DG_OK = 0,
   DG_ERR_INVALID_ARG = 1,    /* a pointer, size or configuration value is out of range   */
-  DG_ERR_OOM = 2,            /* device (or host) allocation failed                        */
+  DG_ERR_OOM = 2,            /* device (or host) allocation failed                      */
   DG_ERR_CAPACITY = 3,       /* batch or sequence length beyond what dg_create reserved   */
   DG_ERR_CUDA = 4,           /* a CUDA runtime call failed (message in dg_last_error)     */
   DG_ERR_DEVICE_TIMEOUT = 5, /* a kernel's bounded wait ran out; outputs are invalid      */

@@ -471,6 +471,10 @@ def test_plan_refuses_misfits():
     bad["block_table"] = [good["block_table"].cpu(), good["block_table"].long(), i32([0, 1]), i32([[0, 1], [2, 3]]).t(),
                           None, i32([[], []])]
     refusals(dg.paged_plan, good, bad)
+    for page in (2 ** 32 + 64, -1, None, "64"):
+        with pytest.raises(dg.DGError) as e:
+            dg.paged_plan(**{**good, "page_size": page})
+        assert e.value.status == dg.DG_ERR_INVALID_ARG and "page_size" in str(e.value)
     with pytest.raises(dg.DGError) as e:
         dg.paged_plan(**{**good, "page_size": 48})
     assert e.value.status == dg.DG_ERR_UNSUPPORTED
@@ -499,6 +503,13 @@ def test_attention_refuses_misfits():
     bad["q"] += [torch.zeros(4, 4, 128, dtype=BF, device="cuda")]
     bad["block_table"] = [good["block_table"].cpu(), good["block_table"].long(), i32([0, 1]), i32([[0, 1], [2, 3]]).t(), None]
     refusals(dg.paged_attention, good, bad)
+    for kw in (dict(max_rows=1.5), dict(max_rows=None), dict(scale=1e39), dict(scale="1"), dict(scale=0.0),
+               dict(scale=math.nan)):
+        with pytest.raises(dg.DGError) as e:
+            dg.paged_attention(**good, **kw)
+        assert e.value.status == dg.DG_ERR_INVALID_ARG, kw
+    dg.paged_attention(**good, max_rows=2 ** 40)                 # a bound above the rows says nothing
+    torch.cuda.synchronize()
 
 
 # ---------------------------------------------------------------------------
