@@ -173,6 +173,26 @@ def test_append_rotates_and_writes_only_its_slots(heads, page, rows, pad):
     assert torch.equal(kk, k0) and torch.equal(vv, v0)                   # nothing else moved
 
 
+def test_append_reaches_pages_beyond_32_bit_offsets():
+    hq, hkv, d = A4B
+    page, rows = 64, 70
+    n_pages = 2 ** 32 // (hkv * page * d) + 40                     # more than 2^32 elements in a pool
+    g = torch.Generator().manual_seed(24)
+    qkv = torch.randn(rows, (hq + 2 * hkv) * d, generator=g).to(BF).cuda()
+    slots = (n_pages - 1 - torch.arange(rows)) * page + torch.arange(rows) % page
+    small = [torch.empty(rows, hkv, page, d, dtype=BF, device="cuda") for _ in range(2)]
+    big = [torch.empty(n_pages, hkv, page, d, dtype=BF, device="cuda") for _ in range(2)]
+    q = [torch.empty(rows, hq, d, dtype=BF, device="cuda") for _ in range(2)]
+    pos, rope = i32(list(range(rows))), dg.rope_table(rows, d)
+    dg.paged_append(qkv, pos, slots.int().cuda(), rope, *big, q[0])
+    near = torch.arange(rows) * page + torch.arange(rows) % page
+    dg.paged_append(qkv, pos, near.int().cuda(), rope, *small, q[1])
+    assert torch.equal(*q)
+    r = torch.arange(rows, device="cuda")
+    for b, s in zip(big, small):
+        assert torch.equal(b[n_pages - 1 - r, :, r % page], s[r, :, r % page])
+
+
 def test_rope_table_has_the_angles_of_far_positions():
     t = dg.rope_table(40000, 176).cpu().double()
     for p, j in [(0, 0), (1, 0), (39999, 0), (39999, 1), (12345, 87), (33023, 3)]:
@@ -285,6 +305,27 @@ def test_attention_over_many_requests(rows):
     g = torch.Generator().manual_seed(4)
     q, k, v, table, cu = paged_cache(g, TINY, 16, kv, [rows] * len(kv))
     check_attention(q, k, v, table, kv, cu, True, max_rows=rows)
+
+
+@pytest.mark.parametrize("batch", [31, 32, 33, 64, 65, 96, 97, 127, 128, 129, 257])
+@pytest.mark.parametrize("most", [1, 70])
+def test_stretches_start_in_the_right_request(batch, most):
+    """batches around the sizes at which the search for a stretch's start changes, requests without rows among them"""
+    rng = random.Random(batch)
+    rows = [rng.choice([0, 1, most, rng.randint(1, most)]) for _ in range(batch)]
+    rows[0], rows[-1] = 0, most
+    kv = [n + rng.choice([0, 0, 15, 64, 130]) for n in rows]
+    g = torch.Generator().manual_seed(batch)
+    q, k, v, table, cu = paged_cache(g, TINY, 16, kv, rows)
+    for causal in (True, False):
+        check_attention(q, k, v, table, kv, cu, causal, max_rows=most)
+
+
+def test_causal_prompts_of_more_than_32_row_tiles():
+    g = torch.Generator().manual_seed(23)
+    kv, rows = [4300, 90, 8400], [4250, 3, 8400]
+    q, k, v, table, cu = paged_cache(g, (2, 1, 64), 64, kv, rows)
+    check_attention(q, k, v, table, kv, cu, True)
 
 
 @pytest.mark.parametrize("rows", [1, 64])

@@ -112,6 +112,56 @@ def test_graph_and_eager_steps_agree_over_blocks():
         assert torch.equal(a, b)
 
 
+def test_entropy_steps_with_self_conditioning_and_host_steps():
+    """graph and eager agree there too, with a regular batch in between (its graphs are others), and a step on host
+    buffers gives what one on the device does"""
+    lens = [100, 1, 333]
+    w = si.workload("tiny").with_(batch=3)
+    results = []
+    for graph in (False, True):
+        st = torch.cuda.Stream()
+        with torch.cuda.stream(st):
+            weights = {**si.model_weights(w, "cuda"), **si.self_cond_weights(w, "cuda")}
+            ctx, _ = make_context(w, max_seq=333 + 3 * 256, weights=weights, stream=st.cuda_stream if graph else None)
+            got = []
+            regular = si.uniform_tokens(w, "prefix", 3, 90).cuda()
+            tokens = packed(prompts(w, lens))
+            canvas = torch.as_tensor(canvas_of(w)).cuda()
+            ctx.set_self_conditioning(True)
+            for ragged in (True, False, True):
+                torch.cuda.synchronize()
+                ctx.prefill_ragged(tokens, lens) if ragged else ctx.prefill(regular)
+                cur, prev = canvas, None
+                for step in range(2):
+                    out, am = torch.empty_like(cur), torch.empty_like(cur)
+                    ent = torch.empty(3, 256, device="cuda")
+                    if not graph:
+                        torch.cuda.synchronize()
+                    ctx.denoise_step_entropy(cur, step, 11, 0.8, 20.0, 0.005, out, prev_argmax=prev, argmax_out=am,
+                                             entropy=ent)
+                    ctx.sync()
+                    got += [out.clone(), am.clone(), ent.clone()]
+                    cur, prev = out, am
+                ctx.commit_block(cur)
+                ctx.sync()
+            ctx.set_self_conditioning(False)
+            out, conf = torch.empty_like(canvas), torch.empty(3, 256, device="cuda")
+            if not graph:
+                torch.cuda.synchronize()
+            ctx.denoise_step(canvas, 1, 5, 0.4, out, conf)
+            ctx.sync()
+            h_out, h_conf = np.zeros((3, 256), np.int32), np.zeros((3, 256), np.float32)
+            ctx.denoise_step_host(canvas_of(w).astype(np.int32), 1, 5, 0.4, h_out, h_conf)
+            np.testing.assert_array_equal(h_out, out.cpu().numpy())
+            np.testing.assert_array_equal(h_conf, conf.cpu().numpy())
+            results.append(got)
+            ctx.close()
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    for a, b in zip(results[0][:6], results[0][12:]):              # the second ragged batch gives what the first did
+        assert torch.equal(a, b)
+
+
 def test_samplers_draw_at_each_sequences_own_positions():
     lens = [16, 200, 77]
     w = si.workload("tiny").with_(batch=3)
