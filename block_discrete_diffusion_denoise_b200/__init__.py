@@ -77,6 +77,20 @@ class dg_entropy_args(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_float), ("gamma", ctypes.c_float), ("stop_entropy", ctypes.c_float)]
 
 
+class dg_paged_plan_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("cached_lens", "new_rows", "block_table", "free_pages", "free_state",
+                                               "cu_rows", "kv_lens", "positions", "slots", "free_state_out")] + \
+               [("table_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("batch", "table_width", "n_pages", "page_size", "row_capacity")]
+
+
+class dg_paged_append_args(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("qkv", "positions", "slots", "rope", "k_pages", "v_pages", "q_out")] + \
+               [("qkv_stride", ctypes.c_int64)] + \
+               [(n, ctypes.c_int32) for n in ("n_rows", "n_q_heads", "n_kv_heads", "head_dim", "n_positions", "n_pages",
+                                              "page_size")]
+
+
 class dg_paged_attention_args(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("q", "k_pages", "v_pages", "block_table", "kv_lens", "cu_rows", "out",
                                                "lse", "workspace")] + \
@@ -136,9 +150,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "dg_debug_timeline_reset": ([P], I32),
         "dg_debug_timeline": ([P, P, I32, ctypes.POINTER(I64)], I32),
         "dg_lmhead_argmax_static": ([P, I32, I32, P, I32, F32, P, P, P, P], I32),
-        "dg_paged_plan": ([P, P, I32, P, I32, I64, P, I32, P, I32, P, P, P, P, I32, P, P], I32),
-        "dg_paged_append": ([P, I64, I32, I32, I32, I32, P, P, P, I32, P, P, I32, I32, P, P], I32),
-        # dg_paged_attention_args by address: byref() of the struct, or its bytes
+        # argument structs by address: byref() of one, or its bytes
+        "dg_paged_plan": ([P, P], I32),
+        "dg_paged_append": ([P, P], I32),
         "dg_paged_attention_workspace": ([P, ctypes.POINTER(I64)], I32),
         "dg_paged_attention": ([P, P], I32),
     }
@@ -511,7 +525,12 @@ def lmhead_argmax_static(z, embed, temperature, argmax=None, lse=None, conf=None
 # torch offers bound to module names; what is wrong with a bad one is found
 # again, condition by condition, in order to say it.
 _BF16 = _I32 = _F32 = _current_device = _raw_stream = None
-_I32_MAX = 2 ** 31 - 1
+
+
+# the argument structs packed without building a ctypes object
+_PAGED_PLAN_ARGS = struct.Struct("@10Pq5i4x")            # dg_paged_plan_args
+_PAGED_APPEND_ARGS = struct.Struct("@7Pq7i4x")           # dg_paged_append_args
+_PAGED_ATTENTION_ARGS = struct.Struct("@9P3q10if4x")     # dg_paged_attention_args
 
 
 def _bind_torch():
@@ -556,14 +575,14 @@ def _paged_check_pools(k_pages, v_pages, idx):
     _paged_check(v_pages, _BF16, "v_pages", want + " like k_pages", idx, shape=k_pages.shape)
 
 
-def _paged_call(f, idx, *args):
-    """The library's f with CUDA device idx current, on torch's current stream there."""
+def _paged_call(f, idx, args):
+    """The library's f on an argument struct's bytes, with CUDA device idx current, on torch's current stream there."""
     if _current_device() == idx:
-        st = f(*args, _raw_stream(idx))
+        st = f(args, _raw_stream(idx))
     else:
         import torch
         with torch.cuda.device(idx):
-            st = f(*args, _raw_stream(idx))
+            st = f(args, _raw_stream(idx))
     if st != DG_OK:
         raise DGError(st, f"{f.__name__} refused (shape, alignment, overlap or capacity; see include/dg.h)")
 
@@ -607,9 +626,13 @@ def paged_plan(cached_lens, new_rows, block_table, free_pages, free_state, page_
                 and free_state.is_contiguous() and cu_rows.is_contiguous() and kv_lens.is_contiguous()
                 and positions.is_contiguous() and slots.is_contiguous() and free_state_out.is_contiguous())
         stride = W if block_table.is_contiguous() else block_table.stride(0)
-        good = (good and (stride == W or block_table.stride(1) == 1 or W == 1)
-                and cap <= _I32_MAX and free_pages.numel() <= _I32_MAX and 0 <= page_size <= _I32_MAX)
-    except (AttributeError, TypeError, ValueError):
+        good = good and (stride == W or block_table.stride(1) == 1 or W == 1)
+        if good:
+            args = _PAGED_PLAN_ARGS.pack(
+                cached_lens.data_ptr(), new_rows.data_ptr(), block_table.data_ptr(), free_pages.data_ptr(),
+                free_state.data_ptr(), cu_rows.data_ptr(), kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(),
+                free_state_out.data_ptr(), stride if B > 1 else W, B, W, free_pages.numel(), page_size, cap)
+    except (AttributeError, ValueError, struct.error):
         good = False
     if not good:
         _paged_check_table(block_table, None)
@@ -621,11 +644,8 @@ def paged_plan(cached_lens, new_rows, block_table, free_pages, free_state, page_
                            (free_state, 2, "free_state"), (cu_rows, B + 1, "cu_rows"), (kv_lens, B, "kv_lens"),
                            (positions, slots.numel(), "positions"), (free_state_out, 4, "free_state_out")):
             _paged_check_ints(t, n, what, idx)
-        _invalid("page_size, or the number of free_pages or slots: expected a number of 32 bits")
-    _paged_call(_lib.dg_paged_plan, idx, cached_lens.data_ptr(), new_rows.data_ptr(), B, block_table.data_ptr(), W,
-                stride if B > 1 else W, free_pages.data_ptr(), free_pages.numel(), free_state.data_ptr(), page_size,
-                cu_rows.data_ptr(), kv_lens.data_ptr(), positions.data_ptr(), slots.data_ptr(), cap,
-                free_state_out.data_ptr())
+        _invalid("page_size, or the number of free_pages or slots: expected an int of 32 bits")
+    _paged_call(_lib.dg_paged_plan, idx, args)
 
 
 def paged_append(qkv, positions, slots, rope, k_pages, v_pages, q_out):
@@ -676,12 +696,11 @@ def paged_append(qkv, positions, slots, rope, k_pages, v_pages, q_out):
         _invalid("arguments")
     if rows == 0:
         return
-    _paged_call(_lib.dg_paged_append, idx, qkv.data_ptr(), stride if rows > 1 else width, rows, hq, hkv, d,
-                positions.data_ptr(), slots.data_ptr(), rope.data_ptr(), n_pos, k_pages.data_ptr(), v_pages.data_ptr(),
-                n_pages, page, q_out.data_ptr())
+    _paged_call(_lib.dg_paged_append, idx, _PAGED_APPEND_ARGS.pack(
+        qkv.data_ptr(), positions.data_ptr(), slots.data_ptr(), rope.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        q_out.data_ptr(), stride if rows > 1 else width, rows, hq, hkv, d, n_pos, n_pages, page))
 
 
-_PAGED_ATTENTION_ARGS = struct.Struct("@9P3q10if4x")     # dg_paged_attention_args
 _paged_workspace_bytes: dict = {}                        # (device, head_dim, group, bound of rows): bytes
 
 

@@ -488,9 +488,23 @@ dg_status ragged_attention(dg_ctx* c, int l, int T, bool causal) {
 dg_status ragged_plan(dg_ctx* c, const std::vector<int32_t>& rows) {
   c->rg_rows = *std::max_element(rows.begin(), rows.end());
   DG_CUDA(c, cudaMemcpyAsync(c->rg_new, rows.data(), rows.size() * 4, cudaMemcpyHostToDevice, c->stream));
-  const dg_status st = dg_paged_plan(c->rg_lens, c->rg_new, c->B, c->rg_table, c->rg_width, c->rg_width, c->rg_ring,
-                                     c->rg_pages, c->rg_state + 4 * c->rg_cur, kRaggedPage, c->rg_cu, c->rg_kv,
-                                     c->rg_pos, c->rg_slots, c->R, c->rg_state + 4 * (c->rg_cur ^ 1), c->stream);
+  dg_paged_plan_args a{};
+  a.cached_lens = c->rg_lens;
+  a.new_rows = c->rg_new;
+  a.block_table = c->rg_table;
+  a.free_pages = c->rg_ring;
+  a.free_state = c->rg_state + 4 * c->rg_cur;
+  a.cu_rows = c->rg_cu;
+  a.kv_lens = c->rg_kv;
+  a.positions = c->rg_pos;
+  a.slots = c->rg_slots;
+  a.free_state_out = c->rg_state + 4 * (c->rg_cur ^ 1);
+  a.table_stride = a.table_width = c->rg_width;
+  a.batch = c->B;
+  a.n_pages = c->rg_pages;
+  a.page_size = kRaggedPage;
+  a.row_capacity = c->R;
+  const dg_status st = dg_paged_plan(&a, c->stream);
   if (st != DG_OK) return fail(c, st, "ragged plan");
   c->launches++;
   return DG_OK;

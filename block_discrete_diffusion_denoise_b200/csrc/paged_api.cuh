@@ -212,95 +212,90 @@ dg_status launch_attention(CanvasParams& cp, bool few, int head_dim, void* works
 
 extern "C" {
 
-dg_status dg_paged_plan(const int32_t* cached, const int32_t* fresh, int32_t batch, int32_t* table, int32_t width,
-                        int64_t table_stride, int32_t* free_pages, int32_t n_pages, const int32_t* free_state,
-                        int32_t page_size, int32_t* cu_rows, int32_t* kv_lens, int32_t* positions, int32_t* slots,
-                        int32_t row_capacity, int32_t* free_state_out, void* cuda_stream) {
-  const int shift = page_shift_of(page_size);
-  if (!cached || !fresh || !table || !free_pages || !free_state || !cu_rows || !kv_lens || !free_state_out ||
-      batch <= 0 || width <= 0 || table_stride < width || n_pages <= 0 || row_capacity < 0 ||
-      (row_capacity > 0 && (!positions || !slots)))
+dg_status dg_paged_plan(const dg_paged_plan_args* a, void* cuda_stream) {
+  if (!a || !a->cached_lens || !a->new_rows || !a->block_table || !a->free_pages || !a->free_state || !a->cu_rows ||
+      !a->kv_lens || !a->free_state_out || a->batch <= 0 || a->table_width <= 0 ||
+      a->table_stride < a->table_width || a->n_pages <= 0 || a->row_capacity < 0 ||
+      (a->row_capacity > 0 && (!a->positions || !a->slots)))
     return DG_ERR_INVALID_ARG;
+  const int shift = page_shift_of(a->page_size);
   if (shift < 0) return DG_ERR_UNSUPPORTED;
-  if (n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;  // a slot is 32 bits
-  const int64_t B = batch;
-  if (operands_clash({{cached, B * 4, false},
-                      {fresh, B * 4, false},
-                      {free_state, 8, false},
-                      {table, ((B - 1) * table_stride + width) * 4, true},
-                      {free_pages, static_cast<int64_t>(n_pages) * 4, true},
-                      {cu_rows, (B + 1) * 4, true},
-                      {kv_lens, B * 4, true},
-                      {positions, static_cast<int64_t>(row_capacity) * 4, true},
-                      {slots, static_cast<int64_t>(row_capacity) * 4, true},
-                      {free_state_out, 16, true}}))
+  if (a->n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;  // a slot is 32 bits
+  const int64_t B = a->batch, cap = a->row_capacity;
+  if (operands_clash({{a->cached_lens, B * 4, false},
+                      {a->new_rows, B * 4, false},
+                      {a->free_state, 8, false},
+                      {a->block_table, ((B - 1) * a->table_stride + a->table_width) * 4, true},
+                      {a->free_pages, a->n_pages * int64_t(4), true},
+                      {a->cu_rows, (B + 1) * 4, true},
+                      {a->kv_lens, B * 4, true},
+                      {a->positions, cap * 4, true},
+                      {a->slots, cap * 4, true},
+                      {a->free_state_out, 16, true}}))
     return DG_ERR_INVALID_ARG;
   PagedPlanParams p;
-  p.cached = cached;
-  p.fresh = fresh;
-  p.table = table;
-  p.table_stride = table_stride;
-  p.ring = free_pages;
-  p.state = free_state;
-  p.cu_rows = cu_rows;
-  p.kv_lens = kv_lens;
-  p.positions = positions;
-  p.slots = slots;
-  p.state_out = free_state_out;
-  p.batch = batch;
-  p.width = width;
-  p.n_pages = n_pages;
+  p.cached = a->cached_lens;
+  p.fresh = a->new_rows;
+  p.table = a->block_table;
+  p.table_stride = a->table_stride;
+  p.ring = a->free_pages;
+  p.state = a->free_state;
+  p.cu_rows = a->cu_rows;
+  p.kv_lens = a->kv_lens;
+  p.positions = a->positions;
+  p.slots = a->slots;
+  p.state_out = a->free_state_out;
+  p.batch = a->batch;
+  p.width = a->table_width;
+  p.n_pages = a->n_pages;
   p.page_shift = shift;
-  p.row_cap = row_capacity;
+  p.row_cap = a->row_capacity;
   // one CTA per request up to a wave of them; strips of a request's rows where
   // there are few requests of many rows
-  const int gx = std::min(batch, 148);
-  const int64_t strips = row_capacity / (static_cast<int64_t>(batch) * 2 * PLAN_THREADS);
+  const int gx = std::min(a->batch, 148);
+  const int64_t strips = cap / (B * 2 * PLAN_THREADS);
   const int gy = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(strips, 148 / gx)));
   return paged_launch(paged_plan_kernel, dim3(gx, gy), PLAN_THREADS, 0, cuda_stream, p);
 }
 
-dg_status dg_paged_append(const void* qkv, int64_t qkv_stride, int32_t n_rows, int32_t n_q_heads, int32_t n_kv_heads,
-                          int32_t head_dim, const int32_t* positions, const int32_t* slots, const float* rope,
-                          int32_t n_positions, void* k_pages, void* v_pages, int32_t n_pages, int32_t page_size,
-                          void* q_out, void* cuda_stream) {
-  if (!qkv || !positions || !slots || !rope || !k_pages || !v_pages || !q_out || n_rows < 0 || n_positions <= 0 ||
-      n_pages <= 0 || !aligned16(qkv) || !aligned16(rope) || !aligned16(k_pages) || !aligned16(v_pages) ||
-      !aligned16(q_out))
+dg_status dg_paged_append(const dg_paged_append_args* a, void* cuda_stream) {
+  if (!a || !a->qkv || !a->positions || !a->slots || !a->rope || !a->k_pages || !a->v_pages || !a->q_out ||
+      a->n_rows < 0 || a->n_positions <= 0 || a->n_pages <= 0 || !aligned16(a->qkv) || !aligned16(a->rope) ||
+      !aligned16(a->k_pages) || !aligned16(a->v_pages) || !aligned16(a->q_out))
     return DG_ERR_INVALID_ARG;
-  const dg_status hs = check_heads(n_q_heads, n_kv_heads, head_dim);
+  const dg_status hs = check_heads(a->n_q_heads, a->n_kv_heads, a->head_dim);
   if (hs != DG_OK) return hs;
-  const int shift = page_shift_of(page_size);
+  const int shift = page_shift_of(a->page_size);
   if (shift < 0) return DG_ERR_UNSUPPORTED;
-  const int heads = n_q_heads + 2 * n_kv_heads;
-  if (qkv_stride < static_cast<int64_t>(heads) * head_dim || qkv_stride % 8) return DG_ERR_INVALID_ARG;
-  if (n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;
-  if (n_rows == 0) return DG_OK;
-  const int64_t rows = n_rows, pool = (static_cast<int64_t>(n_pages) << shift) * n_kv_heads * head_dim * 2;
-  if (operands_clash({{qkv, ((rows - 1) * qkv_stride + static_cast<int64_t>(heads) * head_dim) * 2, false},
-                      {positions, rows * 4, false},
-                      {slots, rows * 4, false},
-                      {rope, static_cast<int64_t>(n_positions) * head_dim * 4, false},
-                      {k_pages, pool, true},
-                      {v_pages, pool, true},
-                      {q_out, rows * n_q_heads * head_dim * 2, true}}))
+  const int64_t rows = a->n_rows, width = (a->n_q_heads + int64_t(2) * a->n_kv_heads) * a->head_dim;
+  if (a->qkv_stride < width || a->qkv_stride % 8) return DG_ERR_INVALID_ARG;
+  if (a->n_pages > (INT32_MAX >> shift)) return DG_ERR_CAPACITY;
+  if (rows == 0) return DG_OK;
+  const int64_t pool = (static_cast<int64_t>(a->n_pages) << shift) * a->n_kv_heads * a->head_dim * 2;
+  if (operands_clash({{a->qkv, ((rows - 1) * a->qkv_stride + width) * 2, false},
+                      {a->positions, rows * 4, false},
+                      {a->slots, rows * 4, false},
+                      {a->rope, static_cast<int64_t>(a->n_positions) * a->head_dim * 4, false},
+                      {a->k_pages, pool, true},
+                      {a->v_pages, pool, true},
+                      {a->q_out, rows * a->n_q_heads * a->head_dim * 2, true}}))
     return DG_ERR_INVALID_ARG;
   PagedAppendParams p{};
-  p.qkv = static_cast<const uint16_t*>(qkv);
-  p.qkv_stride = qkv_stride;
-  p.positions = positions;
-  p.slots = slots;
-  p.rope = reinterpret_cast<const float4*>(rope);
-  p.k = static_cast<uint16_t*>(k_pages);
-  p.v = static_cast<uint16_t*>(v_pages);
-  p.q = static_cast<uint16_t*>(q_out);
-  p.n_slots = static_cast<int64_t>(n_pages) << shift;
-  p.rows = n_rows;
-  p.n_positions = n_positions;
-  p.Hq = n_q_heads;
-  p.Hkv = n_kv_heads;
+  p.qkv = static_cast<const uint16_t*>(a->qkv);
+  p.qkv_stride = a->qkv_stride;
+  p.positions = a->positions;
+  p.slots = a->slots;
+  p.rope = reinterpret_cast<const float4*>(a->rope);
+  p.k = static_cast<uint16_t*>(a->k_pages);
+  p.v = static_cast<uint16_t*>(a->v_pages);
+  p.q = static_cast<uint16_t*>(a->q_out);
+  p.n_slots = static_cast<int64_t>(a->n_pages) << shift;
+  p.rows = a->n_rows;
+  p.n_positions = a->n_positions;
+  p.Hq = a->n_q_heads;
+  p.Hkv = a->n_kv_heads;
   p.page_shift = shift;
-  return launch_append<false>(p, head_dim, cuda_stream);
+  return launch_append<false>(p, a->head_dim, cuda_stream);
 }
 
 dg_status dg_paged_attention_workspace(const dg_paged_attention_args* a, int64_t* bytes) {

@@ -455,47 +455,76 @@ dg_status dg_lmhead_argmax_static(const void* z_dev, int32_t n_rows, int32_t d_m
  * lengths.  With held = ceil(cached / page_size) and need = ceil((cached +
  * new) / page_size), request b takes need - held pages from the pool, or gives
  * held - need back where new_rows is negative (-cached releases it all).
- *   cached_dev, new_dev [batch] int32
- *   block_table_dev     entries [held, need) are written, the others left
- *   free_pages_dev      [n_pages] ring of free page ids; pages are taken from
+ *   cached_lens, new_rows  [batch] int32
+ *   block_table         entries [held, need) are written, the others left
+ *   free_pages          [n_pages] ring of free page ids; pages are taken from
  *                       its head and put behind its tail, in the order of
  *                       request and page
- *   free_state_dev      [2] int32 {index of the ring's head, free pages}
- *   cu_rows_dev         [batch + 1] out: exclusive sums of max(new, 0)
- *   kv_lens_dev         [batch] out: cached + new
- *   positions_dev, slots_dev [row_capacity] out: cached + i and its slot for
+ *   free_state          [2] int32 {index of the ring's head, free pages}
+ *   cu_rows             [batch + 1] out: exclusive sums of max(new, 0)
+ *   kv_lens             [batch] out: cached + new
+ *   positions, slots    [row_capacity] out: cached + i and its slot for
  *                       row i of each request; entries behind the last row
  *                       are left as they were (both may be NULL with
  *                       row_capacity 0)
- *   free_state_out_dev  [4] int32 out: {head, free pages} after the call,
+ *   free_state_out      [4] int32 out: {head, free pages} after the call,
  *                       missing pages, reasons
  * All or nothing: where the free pages do not suffice (missing > 0) or a
  * reason is set (bit 0: a negative length, or new < -cached; bit 1: a request
  * needs more than table_width pages; bit 2: more than row_capacity rows; bit
  * 3: free_state is no state of the ring), no page changes hands, kv_lens
  * is cached and the rows' slots are -1, which dg_paged_append skips.  A call
- * leaves free_state_dev as it was, so it may be made again, or its outcome be
- * dropped, until the next one is given its free_state_out_dev. */
-dg_status dg_paged_plan(const int32_t* cached_dev, const int32_t* new_dev, int32_t batch, int32_t* block_table_dev,
-                        int32_t table_width, int64_t table_stride, int32_t* free_pages_dev, int32_t n_pages,
-                        const int32_t* free_state_dev, int32_t page_size, int32_t* cu_rows_dev,
-                        int32_t* kv_lens_dev, int32_t* positions_dev, int32_t* slots_dev, int32_t row_capacity,
-                        int32_t* free_state_out_dev, void* cuda_stream);
+ * leaves free_state as it was, so it may be made again, or its outcome be
+ * dropped, until the next one is given its free_state_out. */
+typedef struct dg_paged_plan_args {
+  const int32_t* cached_lens;
+  const int32_t* new_rows;
+  int32_t* block_table;
+  int32_t* free_pages;
+  const int32_t* free_state;
+  int32_t* cu_rows;
+  int32_t* kv_lens;
+  int32_t* positions;
+  int32_t* slots;
+  int32_t* free_state_out;
+  int64_t table_stride;
+  int32_t batch;
+  int32_t table_width;
+  int32_t n_pages;
+  int32_t page_size;
+  int32_t row_capacity;
+} dg_paged_plan_args;
+
+dg_status dg_paged_plan(const dg_paged_plan_args* args, void* cuda_stream);
 
 /* Rotary positions on the new rows and their way into the pages: rows
- * qkv_dev [n_rows][(Hq + 2 Hkv) * D] bf16 (query, key, value heads; rows
+ * qkv [n_rows][(Hq + 2 Hkv) * D] bf16 (query, key, value heads; rows
  * qkv_stride elements apart, a multiple of 8) are rotated in pairs (j, j + D/2)
- * by rope_dev [n_positions][D/2][2] fp32 (cos, sin) at positions_dev [n_rows];
- * q_out_dev [n_rows][Hq][D] bf16 receives q, the pages k and v at slots_dev
+ * by rope [n_positions][D/2][2] fp32 (cos, sin) at positions [n_rows];
+ * q_out [n_rows][Hq][D] bf16 receives q, the pages k and v at slots
  * [n_rows].  A row whose slot is outside the pool writes no k and v; a row whose
  * position is outside the table writes none either, and NaN as its q.  The
  * slots of a call must differ from one another (of two rows with one slot,
  * which one's values stay is not defined). */
-dg_status dg_paged_append(const void* qkv_dev, int64_t qkv_stride, int32_t n_rows, int32_t n_q_heads,
-                          int32_t n_kv_heads, int32_t head_dim, const int32_t* positions_dev,
-                          const int32_t* slots_dev, const float* rope_dev, int32_t n_positions, void* k_pages_dev,
-                          void* v_pages_dev, int32_t n_pages, int32_t page_size, void* q_out_dev,
-                          void* cuda_stream);
+typedef struct dg_paged_append_args {
+  const void* qkv;
+  const int32_t* positions;
+  const int32_t* slots;
+  const float* rope;
+  void* k_pages;
+  void* v_pages;
+  void* q_out;
+  int64_t qkv_stride;
+  int32_t n_rows;
+  int32_t n_q_heads;
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t n_positions;
+  int32_t n_pages;
+  int32_t page_size;
+} dg_paged_append_args;
+
+dg_status dg_paged_append(const dg_paged_append_args* args, void* cuda_stream);
 
 /* Arguments of dg_paged_attention.
  *   q           [n_rows][Hq][D] bf16, rows q_stride elements apart (a multiple of 8)

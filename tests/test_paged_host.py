@@ -11,25 +11,30 @@ import block_discrete_diffusion_denoise_b200 as dg
 A = 0x100000          # an aligned address, never dereferenced
 
 
-def test_argument_struct_matches_the_header():
+@pytest.mark.parametrize("name", ["dg_paged_plan_args", "dg_paged_append_args", "dg_paged_attention_args"])
+def test_argument_structs_match_the_header(name):
     import os
     import re
     src = open(os.path.join(os.path.dirname(__file__), "..", "include", "dg.h")).read()
-    body = src[src.index("typedef struct dg_paged_attention_args"):src.index("} dg_paged_attention_args;")]
-    fields = re.findall(r"(const void\*|const int32_t\*|void\*|float\*|int64_t|int32_t|float)\s+([a-z_]+);", body)
+    body = src[src.index("typedef struct %s {" % name):src.index("} %s;" % name)]
+    fields = re.findall(r"(const void\*|const int32_t\*|const float\*|int32_t\*|void\*|float\*|int64_t|int32_t|float)"
+                        r"\s+([a-z_]+);", body)
     want = [(n, {"int64_t": ctypes.c_int64, "int32_t": ctypes.c_int32, "float": ctypes.c_float}.get(t, ctypes.c_void_p))
             for t, n in fields]
-    assert want == list(dg.dg_paged_attention_args._fields_)
+    assert want == list(getattr(dg, name)._fields_)
 
 
-def test_packed_arguments_match_the_struct():
-    """the binding packs dg_paged_attention_args without building the ctypes object"""
-    fields = dg.dg_paged_attention_args._fields_
-    values = list(range(1, len(fields))) + [0.5]
-    packed = dg._PAGED_ATTENTION_ARGS.pack(*values)
-    assert len(packed) == ctypes.sizeof(dg.dg_paged_attention_args)
-    s = dg.dg_paged_attention_args.from_buffer_copy(packed)
-    assert [getattr(s, n) for n, _ in fields] == values
+@pytest.mark.parametrize("packer,name", [(dg._PAGED_PLAN_ARGS, "dg_paged_plan_args"),
+                                         (dg._PAGED_APPEND_ARGS, "dg_paged_append_args"),
+                                         (dg._PAGED_ATTENTION_ARGS, "dg_paged_attention_args")])
+def test_packed_arguments_match_the_structs(packer, name):
+    """the binding packs the argument structs without building the ctypes objects"""
+    cls = getattr(dg, name)
+    values = [0.5 if t is ctypes.c_float else i + 1 for i, (_, t) in enumerate(cls._fields_)]
+    packed = packer.pack(*values)
+    assert len(packed) == ctypes.sizeof(cls)
+    s = cls.from_buffer_copy(packed)
+    assert [getattr(s, n) for n, _ in cls._fields_] == values
 
 
 def plan(**kw):
@@ -37,9 +42,10 @@ def plan(**kw):
              state=A + 0x4000, page=64, cu=A + 0x5000, kv=A + 0x6000, pos=A + 0x7000, slots=A + 0x8000, cap=10,
              out=A + 0x9000)
     a.update(kw)
-    return dg.load_library().dg_paged_plan(a["cached"], a["new"], a["batch"], a["table"], a["width"], a["stride"],
-                                           a["ring"], a["n_pages"], a["state"], a["page"], a["cu"], a["kv"], a["pos"],
-                                           a["slots"], a["cap"], a["out"], None)
+    args = dg.dg_paged_plan_args(a["cached"], a["new"], a["table"], a["ring"], a["state"], a["cu"], a["kv"], a["pos"],
+                                 a["slots"], a["out"], a["stride"], a["batch"], a["width"], a["n_pages"], a["page"],
+                                 a["cap"])
+    return dg.load_library().dg_paged_plan(ctypes.byref(args), None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -59,9 +65,9 @@ def append(**kw):
     a = dict(qkv=A, stride=5632, rows=4, hq=16, hkv=8, d=176, pos=A + 0x20000, slots=A + 0x21000, rope=A + 0x22000,
              n_pos=100, k=A + 0x1000000, v=A + 0x2000000, n_pages=10, page=64, q=A + 0x40000)
     a.update(kw)
-    return dg.load_library().dg_paged_append(a["qkv"], a["stride"], a["rows"], a["hq"], a["hkv"], a["d"], a["pos"],
-                                             a["slots"], a["rope"], a["n_pos"], a["k"], a["v"], a["n_pages"], a["page"],
-                                             a["q"], None)
+    args = dg.dg_paged_append_args(a["qkv"], a["pos"], a["slots"], a["rope"], a["k"], a["v"], a["q"], a["stride"],
+                                   a["rows"], a["hq"], a["hkv"], a["d"], a["n_pos"], a["n_pages"], a["page"])
+    return dg.load_library().dg_paged_append(ctypes.byref(args), None)
 
 
 @pytest.mark.parametrize("kw,status", [
@@ -99,6 +105,11 @@ def attention(**kw):
 ])
 def test_attention_refuses(kw, status):
     assert attention(**kw) == status
+
+
+@pytest.mark.parametrize("name", ["dg_paged_plan", "dg_paged_append", "dg_paged_attention"])
+def test_no_arguments_are_refused(name):
+    assert getattr(dg.load_library(), name)(None, None) == dg.DG_ERR_INVALID_ARG
 
 
 def refused(fn, *a, **kw):
