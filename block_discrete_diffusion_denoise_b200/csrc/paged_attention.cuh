@@ -7,10 +7,11 @@
 // Work is counted in units: one 64-key block of one tile (packed rows of one
 // request and kv head).  The units of a call form one line, in the order
 // (request, row tile, kv head, key block), and the CTAs take stretches of equal
-// length of it: every CTA has the same work whatever the requests' lengths, and the lengths are read on the device, so a captured launch serves any.  A
-// tile that a stretch cuts leaves its raw rows and row statistics in a
-// partial slot (two per CTA: the stretch's first tile and its last), and
-// the merge kernel joins them in key order.
+// length of it: every CTA has the same work whatever the requests' lengths, and
+// the lengths are read on the device, so a captured launch serves any.  A tile
+// that a stretch cuts leaves its raw rows and row statistics in a partial slot
+// (two per CTA: the stretch's first tile and its last), and the merge kernel
+// joins them in key order.
 #pragma once
 
 #include "paged.cuh"
@@ -417,9 +418,10 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // 64 keys each, with running maxima, sums and rows of their own (no barrier
 // between them inside a tile); at a tile's end they leave these in shared
 // memory and go on, and a warp of its own joins them.
-// One token for 64 requests of 256..8190 keys, 16/8 heads of 176: 233 us with
-// the merge, 6.6 TB/s (1.0 of the copy peak); one request of 2048 keys: 9.1 us,
-// of which the two blocks of a CTA are one.
+// One token for 64 requests of 256..8190 keys, 16/8 heads of 176: 234 us with
+// the merge, 6.6 TB/s (1.0 of the copy peak); 33 requests of up to 1500 keys, 8/2
+// heads of 128: 13.2 us; one request of 2048 keys: 9.3 us, of which the two blocks
+// of a CTA are one.
 // ----------------------------------------------------------------------------
 constexpr int TOK_ROWS = 16;
 constexpr int TOK_WARPS = 4;                       // consumer warps
@@ -650,7 +652,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
         float sum = 0.f;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          // p enters the second product in bf16 (2^-9 of each, averaging out over keys); its sum stays fp32
+          // p enters the second product in bf16 (off by up to 2^-8 of each, averaging out over keys); its sum stays fp32
           const float p0 = ex2_approx(sc[t][2 * x] - base), p1 = ex2_approx(sc[t][2 * x + 1] - base);
           sum += p0 + p1;
           pf[2 * t + x] = cvt_bf16x2(p0, p1);

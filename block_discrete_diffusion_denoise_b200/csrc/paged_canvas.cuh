@@ -14,9 +14,9 @@
 // which keys the producers found.  At D = 176 a unit's products take 1777
 // cycles (48.6 per k-step of S, where both operands come from shared memory and
 // Q is read again for each, 88.5 of P V) and a unit 2050 to 2100.  A canvas of
-// 256 rows over 33,024 keys, 16/8 heads of 176: 97 us with the merge, 980
-// TFLOP/s (114 us once the power limit lowers the clock); eight canvases over
-// 1.5k..6.5k keys 116 us; one over 2304 keys 21.8 us.
+// 256 rows over 33,024 keys, 16/8 heads of 176: 95 us with the merge, 1000
+// TFLOP/s (115 us once the power limit lowers the clock); eight canvases over
+// 1.5k..6.5k keys 112 us; one over 2304 keys 21.5 us.
 #pragma once
 
 #include "paged_attention.cuh"
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
           uint32_t pk[4];
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            // p enters the second product in bf16 (2^-9 of each, averaging out over keys); its sum stays fp32
+            // p enters the second product in bf16 (off by up to 2^-8 of each, averaging out over keys); its sum stays fp32
             float x0, x1;
             f32x2_split(f32x2_fma(f32x2(s[8 * ch + 2 * c], s[8 * ch + 2 * c + 1]), scale2, base2), x0, x1);
             const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
