@@ -263,7 +263,8 @@ class Context:
     lifetime of the context.  Every call runs on `stream` (a cudaStream_t
     handle, e.g. torch.cuda.Stream().cuda_stream; None is the legacy default
     stream, on which steps are not captured into a graph): make inputs on it
-    (torch.cuda.stream(...)) or make it wait for the stream that did."""
+    (torch.cuda.stream(...)) or make it wait for the stream that did.
+    generate_blocks orders its own tensors and calls by itself."""
 
     # where the context's buffers must live (the tests of the argument checks
     # set "cpu" on an instance that never reaches the library)
@@ -272,6 +273,7 @@ class Context:
     def __init__(self, cfg: dict, weights: dict, stream=None):
         self.lib = load_library()
         self._batch = None            # batch of the last successful prefill
+        self._stream = int(getattr(stream, "value", stream) or 0)
         check_weights(cfg, weights, self._device_type)
         self._weights = weights
         c = dg_config()
@@ -316,6 +318,23 @@ class Context:
     # launched.  Before the first prefill the library itself refuses the call.
     def _n(self) -> int:
         return 0 if self._batch is None else self._batch * int(self.cfg["canvas"])
+
+    def _behind_torch(self, *tensors):
+        """Order the calls that follow behind what torch's current stream has
+        been given so far, and have torch keep the memory of `tensors`, which
+        those calls work on, until the context's stream is done with it."""
+        if self._device_type != "cuda":
+            return
+        import torch
+        dev = self._weights["embed"].device
+        theirs = torch.cuda.current_stream(dev)
+        if theirs.cuda_stream == self._stream:
+            return
+        mine = torch.cuda.ExternalStream(self._stream, dev) if self._stream else torch.cuda.default_stream(dev)
+        mine.wait_stream(theirs)
+        for t in tensors:
+            if t.is_cuda:             # the call itself refuses any other
+                t.record_stream(mine)
 
     def _dev(self, t, dtype, n, what, optional=False):
         _check_tensor(t, dtype, n, what, self._device_type, optional=optional)
@@ -825,16 +844,23 @@ def generate_blocks(ctx: Context, prefix, init_canvas, n_blocks: int, max_steps:
     (tests use them to record a step; with the entropy sampler conf holds the
     entropies and settled the stop flags).  Host control only: every step of the
     path runs in the library's kernels; the one device-to-host read per step is
-    the batch's all-settled flags.
+    the batch's all-settled flags.  The context's stream need not be torch's
+    current one: it waits for what the current one was given (prefix and
+    canvases among it) before each call.
 
     Returns {"blocks": [final canvas of each block], "steps": [steps taken per
     block], "settled": [whether each block stopped early]}."""
     import torch
     ragged = isinstance(prefix, (list, tuple))
     B, C = (len(prefix) if ragged else int(prefix.shape[0])), int(ctx.cfg["canvas"])
+    # the tensors made here belong to torch's current stream, the calls run on the context's (a stand-in has none)
+    behind_torch = getattr(ctx, "_behind_torch", lambda *tensors: None)
     if ragged:
-        ctx.prefill_ragged(torch.cat([p.reshape(-1) for p in prefix]), [p.numel() for p in prefix])
+        packed = torch.cat([p.reshape(-1) for p in prefix])
+        behind_torch(packed)
+        ctx.prefill_ragged(packed, [p.numel() for p in prefix])
     else:
+        behind_torch()
         ctx.prefill(prefix)
     out = {"blocks": [], "steps": [], "settled": []}
     for k in range(n_blocks):
@@ -847,6 +873,7 @@ def generate_blocks(ctx: Context, prefix, init_canvas, n_blocks: int, max_steps:
         for s in range(max_steps):
             if before_step is not None:
                 before_step(k, s)
+            behind_torch(cur, nxt, conf, settled, argmax)
             if entropy is not None:
                 ctx.denoise_step_entropy(cur, s, seed, anneal_temperature(s, max_steps), entropy["gamma"],
                                          entropy["stop_entropy"], nxt, prev_argmax=argmax if s > 0 else None,

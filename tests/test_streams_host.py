@@ -1,0 +1,84 @@
+"""The order of torch's streams and a context's, without a device: what
+generate_blocks makes on torch's current stream is waited for before the
+context's next call, and its memory is kept until the context is done with it."""
+import pytest
+import torch
+
+import block_discrete_diffusion_denoise_b200 as dg
+
+from test_binding_checks import _host_context, _i32
+
+
+class Ordered(dg.Context):
+    """A context on the host that writes down what it is told to wait for, between the library's calls."""
+
+    def _behind_torch(self, *tensors):
+        self.lib.calls.append(("wait", tensors))
+
+
+def ordered():
+    ctx = _host_context()
+    ctx.__class__ = Ordered
+    return ctx
+
+
+@pytest.mark.parametrize("entropy", [None, {"gamma": 1.0, "stop_entropy": 0.1}])
+@pytest.mark.parametrize("prefix", [_i32(2, 5), [_i32(5), _i32(1, 9)]])
+def test_every_call_of_generate_blocks_follows_the_tensors_it_works_on(prefix, entropy):
+    ctx = ordered()
+    given = {}
+
+    def watch(name, *at):
+        inner = getattr(ctx, name)
+
+        def call(*a, **kw):
+            last = ctx.lib.calls[-1]
+            assert last[0] == "wait", name
+            tensors = [x for x in list(a) + list(kw.values()) if isinstance(x, torch.Tensor)]
+            given.setdefault(name, []).append((tensors, last[1]))
+            return inner(*a, **kw)
+        setattr(ctx, name, call)
+    for name in ("prefill", "prefill_ragged", "denoise_step", "denoise_step_entropy"):
+        watch(name)
+    dg.generate_blocks(ctx, prefix, lambda k: _i32(2, 256), 2, 2, 0.9, 0, entropy=entropy)
+    for name, calls in given.items():
+        for used, kept in calls:
+            if name != "prefill":                 # the caller keeps its own prefix
+                assert all(any(t is k for k in kept) for t in used), name
+    assert set(given) == {"prefill_ragged" if isinstance(prefix, list) else "prefill",
+                          "denoise_step" if entropy is None else "denoise_step_entropy"}
+
+
+class Stream:
+    def __init__(self, handle):
+        self.cuda_stream, self.waited = handle, []
+
+    def wait_stream(self, other):
+        self.waited.append(other)
+
+
+class Tensor:
+    is_cuda = True
+
+    def __init__(self):
+        self.kept = []
+
+    def record_stream(self, s):
+        self.kept.append(s)
+
+
+@pytest.mark.parametrize("handle", [0, 77])
+def test_the_contexts_stream_waits_for_the_current_one_and_keeps_the_memory(handle, monkeypatch):
+    ctx = _host_context()
+    ctx._device_type, ctx._stream, ctx._weights = "cuda", handle, {"embed": torch.zeros(1)}
+    mine, current = Stream(handle), Stream(42)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda dev: current)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, dev: mine if h == handle else None)
+    monkeypatch.setattr(torch.cuda, "default_stream", lambda dev: mine if handle == 0 else None)
+    t, host = Tensor(), torch.zeros(1)
+    ctx._behind_torch(t, host)
+    assert mine.waited == [current] and t.kept == [mine]
+    # on its own stream there is nothing to order
+    current.cuda_stream = handle
+    ctx._behind_torch(t)
+    assert mine.waited == [current] and t.kept == [mine]
