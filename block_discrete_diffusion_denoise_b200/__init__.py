@@ -842,7 +842,8 @@ def generate_blocks(ctx: Context, prefix, init_canvas, n_blocks: int, max_steps:
     reports the adaptive stop (section 3.3).  before_step(k, s) and
     after_step(k, s, canvas_in, canvas_out, conf, settled) are optional hooks
     (tests use them to record a step; with the entropy sampler conf holds the
-    entropies and settled the stop flags).  Host control only: every step of the
+    entropies and settled the stop flags); the step is finished when after_step
+    runs.  Host control only: every step of the
     path runs in the library's kernels; the one device-to-host read per step is
     the batch's all-settled flags.  The context's stream need not be torch's
     current one: it waits for what the current one was given (prefix and
@@ -881,11 +882,11 @@ def generate_blocks(ctx: Context, prefix, init_canvas, n_blocks: int, max_steps:
             else:
                 t = tau(s) if callable(tau) else tau
                 ctx.denoise_step(cur, s, seed, t, nxt, conf, settled)
+            ctx.sync()                       # canvas, confidences and flags are written on the context's stream
             if after_step is not None:
                 after_step(k, s, cur, nxt, conf, settled)
             cur, nxt = nxt, cur
             steps += 1
-            ctx.sync()                       # the flags are written on the context's stream
             if bool((settled.cpu() != 0).all()):
                 done = True
                 break

@@ -49,6 +49,16 @@ def test_every_call_of_generate_blocks_follows_the_tensors_it_works_on(prefix, e
                           "denoise_step" if entropy is None else "denoise_step_entropy"}
 
 
+@pytest.mark.parametrize("entropy", [None, {"gamma": 1.0, "stop_entropy": 0.1}])
+def test_a_step_is_finished_when_its_hook_runs(entropy):
+    ctx = _host_context()
+    seen = []
+    dg.generate_blocks(ctx, _i32(2, 5), lambda k: _i32(2, 256), 1, 2, 0.9, 0, entropy=entropy,
+                       after_step=lambda *a: seen.append(list(ctx.lib.calls)))
+    name = "dg_denoise_step" if entropy is None else "dg_denoise_step_entropy"
+    assert len(seen) >= 1 and all(calls[-2:] == [name, "dg_sync"] for calls in seen)
+
+
 class Stream:
     def __init__(self, handle):
         self.cuda_stream, self.waited = handle, []
