@@ -56,10 +56,10 @@ struct PagedRequest {
 };
 
 template <int ROWS>
-__device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams& p, int b) {
+__host__ __device__ __forceinline__ PagedRequest paged_request(const PagedAttnParams& p, int b) {
   PagedRequest r;
   r.t0 = min(max(p.cu_rows[b], 0), p.rows);
-  r.n = max(min(p.cu_rows[b + 1], p.rows) - r.t0, 0);
+  r.n = min(max(p.cu_rows[b + 1], r.t0), p.rows) - r.t0;   // within the call whatever the entry, and no overflow
   const int len = max(p.kv_lens[b], 0);
   r.kv = min(len, p.width << p.page_shift);
   r.before = len - r.n;

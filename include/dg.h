@@ -574,11 +574,13 @@ dg_status dg_paged_attention_workspace(const dg_paged_attention_args* args, int6
  * "DiffusionGemma architecture", section 3.2: a canvas over the cache and
  * itself, or the causal encoder), for anything from one row per request to
  * whole prompts.  Rows outside [cu_rows[0], cu_rows[batch]) are left as they
- * were; cu_rows must not decrease.  Keys beyond table_width pages, and keys of
- * a page id outside the pool, are masked; a row that sees no key gets zeros
- * and lse = -inf.  What lies in the pages behind a request's keys (NaN
- * included) has no effect; a NaN or infinite value among a request's own keys
- * may reach all of its rows, those that do not see it too.  If a bounded wait inside the kernel ran out, the
+ * were; cu_rows must not decrease (of entries that do, or that lie outside the
+ * call, a request gets the rows [cu_rows[b], cu_rows[b + 1]) that there are).
+ * Keys beyond table_width pages, and keys of a page id outside the pool, are
+ * masked; a row that sees no key gets zeros and lse = -inf.  What lies in the
+ * pages behind a request's keys (NaN included) has no effect; a NaN or infinite
+ * value among a request's own keys may reach all of its rows, those that do not
+ * see it too.  If a bounded wait inside the kernel ran out, the
  * rows it should have computed come back NaN. */
 dg_status dg_paged_attention(const dg_paged_attention_args* args, void* cuda_stream);
 
