@@ -172,6 +172,7 @@ def _ptr(t) -> int | None:
 
 DG_ERR_INVALID_ARG = 1
 DG_ERR_UNSUPPORTED = 7
+INT32_MAX = 2 ** 31 - 1      # ctypes would cut a larger number off
 
 
 def _invalid(msg: str):
@@ -345,6 +346,8 @@ class Context:
         if getattr(tokens, "dim", lambda: 0)() != 2:
             _invalid("prefill: tokens must be a [batch, prefix_len] tensor")
         B, P = tokens.shape
+        if max(B, P) > INT32_MAX:
+            _invalid("prefill: batch and prefix_len have 32 bits")
         self._check(self.lib.dg_prefill(self.ctx, self._dev(tokens, torch.int32, B * P, "tokens"), B, P))
         self._batch = int(B)
 
@@ -357,6 +360,8 @@ class Context:
         lens = [int(n) for n in lens]
         if getattr(tokens, "dim", lambda: 0)() != 1 or not lens or min(lens) < 1:
             _invalid("prefill_ragged: tokens must be a [sum of lens] tensor, every length at least 1")
+        if max(lens) > INT32_MAX:
+            _invalid("prefill_ragged: a length has 32 bits")
         self._check(self.lib.dg_prefill_ragged(self.ctx, self._dev(tokens, torch.int32, sum(lens), "tokens"),
                                                len(lens), (ctypes.c_int32 * len(lens))(*lens)))
         self._batch = len(lens)

@@ -1344,7 +1344,7 @@ dg_status dg_destroy(dg_ctx* c) {
 dg_status dg_prefill(dg_ctx* c, const int32_t* tokens, int32_t B, int32_t P) {
   if (!c) return DG_ERR_INVALID_ARG;
   if (!tokens || B <= 0 || P <= 0) return fail(c, DG_ERR_INVALID_ARG, "prefill: bad arguments");
-  if (B > c->cfg.max_batch || P + c->cfg.canvas > c->cfg.max_seq)
+  if (B > c->cfg.max_batch || P > c->cfg.max_seq - c->cfg.canvas)
     return fail(c, DG_ERR_CAPACITY, "prefill: batch %d / length %d beyond capacity", B, P);
   c->B = B;
   c->P = 0;
