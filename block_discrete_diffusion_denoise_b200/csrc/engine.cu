@@ -1614,7 +1614,9 @@ dg_status dg_debug_router(dg_ctx* c, const float* logits, int32_t n_rows, int32_
 
 dg_status dg_debug_sample(dg_ctx* c, const int32_t* argmax, const float* conf, int32_t B, int32_t step,
                           uint64_t seed, float tau, int32_t* out) {
-  if (!c || !argmax || !conf || !out || B <= 0) return fail(c, DG_ERR_INVALID_ARG, "debug_sample");
+  // a ragged batch has a length for each of its own sequences, and no more
+  if (!c || !argmax || !conf || !out || B <= 0 || (c->ragged && B > c->B))
+    return fail(c, DG_ERR_INVALID_ARG, "debug_sample");
   const int T = B * c->cfg.canvas;
   sample_only_kernel<<<(T + 255) / 256, 256, 0, c->stream>>>(argmax, conf, T, c->cfg.canvas, c->P,
                                                               c->ragged ? c->rg_lens : nullptr, step,
@@ -1627,7 +1629,7 @@ dg_status dg_debug_sample(dg_ctx* c, const int32_t* argmax, const float* conf, i
 dg_status dg_debug_entropy_sample(dg_ctx* c, const int32_t* argmax, const float* entropy, const int32_t* prev,
                                   int32_t B, int32_t step, uint64_t seed, float gamma, float stop_entropy,
                                   int32_t* out, int32_t* stopped) {
-  if (!c || !argmax || !entropy || !out || B <= 0 || B > c->cfg.max_batch)
+  if (!c || !argmax || !entropy || !out || B <= 0 || B > (c->ragged ? c->B : c->cfg.max_batch))
     return fail(c, DG_ERR_INVALID_ARG, "debug_entropy_sample");
   EntropyArgs a;
   memset(&a, 0, sizeof(a));

@@ -284,12 +284,13 @@ dg_status dg_debug_router(dg_ctx* ctx, const float* logits_dev, int32_t n_rows, 
                           float* gates_dev);
 
 /* Sampler decision alone on given argmax/conf [batch*canvas] (positions
- * P + i of the current cache length). */
+ * P + i of the current cache length; in a ragged batch of each sequence's, and
+ * batch is at most the batch's). */
 dg_status dg_debug_sample(dg_ctx* ctx, const int32_t* argmax_dev, const float* conf_dev,
                           int32_t batch, int32_t step, uint64_t seed, float tau, int32_t* out_dev);
 
 /* Entropy sampler decision alone on given argmax / entropy [batch*canvas]
- * (positions P + i of the current cache length), prev_argmax or NULL:
+ * (positions and batch as there; at most max_batch), prev_argmax or NULL:
  * out_dev [batch*canvas] int32, stopped_dev [batch] int32 or NULL. */
 dg_status dg_debug_entropy_sample(dg_ctx* ctx, const int32_t* argmax_dev, const float* entropy_dev,
                                   const int32_t* prev_argmax_dev, int32_t batch, int32_t step, uint64_t seed,
