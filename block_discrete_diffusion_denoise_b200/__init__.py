@@ -36,7 +36,7 @@ EXPORTS = ["dg_create", "dg_destroy", "dg_prefill", "dg_denoise_step", "dg_denoi
 TIMELINE_KERNELS = {10: "gemm_dense", 11: "gemm_moe", 13: "gemm_lmhead", 20: "attention", 21: "attn_merge", 30: "route_dispatch",
                     31: "combine_norm", 32: "embed_norm", 33: "residual_norm", 34: "reduce_splits",
                     35: "swiglu_splits", 36: "rope_qkv", 37: "lmhead_merge_sample", 38: "entropy_sample",
-                    39: "router_topk", 40: "sample_only", 50: "other"}
+                    39: "router_topk", 40: "sample_only", 41: "paged_plan", 42: "paged_append", 50: "other"}
 
 # kernel classes of dg_debug_profile (DG_PROF_* in dg.h)
 PROF_CLASSES = ["experts", "routing", "lm_head", "attention", "dense_proj", "other"]

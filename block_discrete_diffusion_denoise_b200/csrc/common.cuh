@@ -35,7 +35,8 @@ __device__ __forceinline__ void raise_error(const DevErr& e, int code) {
 // start and end times (%globaltimer), so the host can rebuild the launch
 // sequence of a graph replay, each launch's span and the gaps between
 // launches without a profiler.  The record is taken when thread 0 leaves the
-// kernel.
+// kernel.  A kernel that may start while the one before it runs opens its scope
+// behind its wait, so that launches do not overlap here either.
 // ----------------------------------------------------------------------------
 enum TimelineKernel : int {
   TLK_GEMM = 10,  // + the GEMM mode (10 dense, 11 expert, 13 LM head)
@@ -52,6 +53,8 @@ enum TimelineKernel : int {
   TLK_ENTROPY_SAMPLE = 38,
   TLK_ROUTER_TOPK = 39,
   TLK_SAMPLE_ONLY = 40,
+  TLK_PAGED_PLAN = 41,
+  TLK_PAGED_APPEND = 42,
   TLK_OTHER = 50,
 };
 

@@ -1711,15 +1711,15 @@ dg_status dg_debug_gemm(dg_ctx* c, const void* w, int32_t M, int32_t K, const vo
 
 constexpr bool timeline_ids_match() {
   using namespace dg;
-  const int ours[17] = {TLK_GEMM + GEMM_DENSE, TLK_GEMM + GEMM_MOE, TLK_GEMM + GEMM_LMHEAD, TLK_ATTENTION, TLK_ATTN_MERGE,
+  const int ours[19] = {TLK_GEMM + GEMM_DENSE, TLK_GEMM + GEMM_MOE, TLK_GEMM + GEMM_LMHEAD, TLK_ATTENTION, TLK_ATTN_MERGE,
                         TLK_ROUTE_DISPATCH, TLK_COMBINE_NORM, TLK_EMBED_NORM, TLK_RESIDUAL_NORM, TLK_REDUCE_SPLITS,
                         TLK_SWIGLU_SPLITS, TLK_ROPE_QKV, TLK_LMHEAD_MERGE_SAMPLE, TLK_ENTROPY_SAMPLE, TLK_ROUTER_TOPK,
-                        TLK_SAMPLE_ONLY, TLK_OTHER};
-  const int abi[17] = {DG_K_GEMM_DENSE, DG_K_GEMM_MOE, DG_K_GEMM_LMHEAD, DG_K_ATTENTION, DG_K_ATTN_MERGE, DG_K_ROUTE_DISPATCH,
+                        TLK_SAMPLE_ONLY, TLK_PAGED_PLAN, TLK_PAGED_APPEND, TLK_OTHER};
+  const int abi[19] = {DG_K_GEMM_DENSE, DG_K_GEMM_MOE, DG_K_GEMM_LMHEAD, DG_K_ATTENTION, DG_K_ATTN_MERGE, DG_K_ROUTE_DISPATCH,
                        DG_K_COMBINE_NORM, DG_K_EMBED_NORM, DG_K_RESIDUAL_NORM, DG_K_REDUCE_SPLITS, DG_K_SWIGLU_SPLITS,
                        DG_K_ROPE_QKV, DG_K_LMHEAD_MERGE_SAMPLE, DG_K_ENTROPY_SAMPLE, DG_K_ROUTER_TOPK,
-                       DG_K_SAMPLE_ONLY, DG_K_OTHER};
-  for (int i = 0; i < 17; ++i)
+                       DG_K_SAMPLE_ONLY, DG_K_PAGED_PLAN, DG_K_PAGED_APPEND, DG_K_OTHER};
+  for (int i = 0; i < 19; ++i)
     if (ours[i] != abi[i]) return false;
   return true;
 }

@@ -85,12 +85,12 @@ __device__ __forceinline__ PlanRequest plan_request(const PagedPlanParams& p, in
 }
 
 __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_constant__ PagedPlanParams p) {
-  DG_TIMELINE_SCOPE(TLK_OTHER);
   __shared__ long long red[7][PLAN_THREADS / 32];
   const int b0 = static_cast<int>(static_cast<int64_t>(blockIdx.x) * p.batch / gridDim.x);
   const int b1 = static_cast<int>(static_cast<int64_t>(blockIdx.x + 1) * p.batch / gridDim.x);
   pdl_launch_dependents();
   pdl_wait();
+  DG_TIMELINE_SCOPE(TLK_PAGED_PLAN);
   // sums before b0 (rows, grow, back), over the batch (rows, grow, back), bad bits
   long long v[7] = {0, 0, 0, 0, 0, 0, 0};
   for (int b = threadIdx.x; b < p.batch; b += PLAN_THREADS) {
@@ -248,13 +248,13 @@ struct AppendIn<false> {
 
 template <int D, bool SPLITS>
 __global__ void __launch_bounds__(APPEND_THREADS) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
-  DG_TIMELINE_SCOPE(TLK_OTHER);
   constexpr int HALF = D / 2, C = HALF / 8;  // chunks of eight pairs in a head
   static_assert(HALF % 8 == 0, "16-byte halves");
   const int heads = p.Hq + 2 * p.Hkv, groups = (heads + APPEND_HEADS - 1) / APPEND_HEADS;
   const int64_t it = static_cast<int64_t>(blockIdx.x) * APPEND_THREADS + threadIdx.x;
   pdl_launch_dependents();
   pdl_wait();
+  DG_TIMELINE_SCOPE(TLK_PAGED_APPEND);
   if (it >= static_cast<int64_t>(p.rows) * groups * C) return;
   const int c = static_cast<int>(it % C);
   const int h0 = static_cast<int>(it / C % groups) * APPEND_HEADS;

@@ -488,7 +488,6 @@ __device__ void paged_poison(const PagedAttnParams& p, const PagedRange& g) {
 
 template <int D>
 __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __grid_constant__ PagedAttnParams p) {
-  DG_TIMELINE_SCOPE(TLK_ATTENTION);
   using C = TokCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -520,6 +519,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
     fence_mbar_init();
   }
   pdl_wait();
+  DG_TIMELINE_SCOPE(TLK_ATTENTION);
   const PagedRange g = paged_range<TOK_ROWS, TOK_THREADS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
   paged_list_none(p, g);
   bool ok = true;
@@ -803,12 +803,12 @@ struct MergeAcc {
 
 template <int ROWS, int D>
 __global__ void __launch_bounds__(MergeCfg<ROWS>::THREADS) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
-  DG_TIMELINE_SCOPE(TLK_ATTN_MERGE);
   using C = MergeCfg<ROWS>;
   __shared__ float4 s_o[ROWS == 16 ? C::THREADS : 1];
   __shared__ float2 s_ml[ROWS == 16 ? C::THREADS : 1];
   pdl_launch_dependents();
   pdl_wait();
+  DG_TIMELINE_SCOPE(TLK_ATTN_MERGE);
   // by tile, the first entry says how many there are (both are fetched at once)
   const int tiles = p.cuts[0].tiles;
   const PagedCut cut = p.cuts[blockIdx.x];

@@ -119,7 +119,6 @@ __device__ __forceinline__ uint64_t f32x2_add(uint64_t a, uint64_t b) {
 }
 template <int D>
 __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __grid_constant__ CanvasParams cp) {
-  DG_TIMELINE_SCOPE(TLK_ATTENTION);
   using C = CvCfg<D>;
   const PagedAttnParams& p = cp.a;
   extern __shared__ uint8_t smem_raw[];
@@ -175,6 +174,7 @@ __global__ void __launch_bounds__(CV_THREADS, 1) paged_canvas_kernel(const __gri
   }
   tc_fence_before();
   pdl_wait();
+  DG_TIMELINE_SCOPE(TLK_ATTENTION);
   const PagedRange g = paged_range<CV_ROWS, CV_THREADS>(p, blockIdx.x, gridDim.x);  // synchronises the CTA
   paged_list_none(p, g);
   tc_fence_after();

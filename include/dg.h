@@ -344,8 +344,9 @@ int64_t dg_debug_launch_count(const dg_ctx* ctx);
  * -DDG_TIMELINE: thread 0 of every CTA of every kernel appends one record
  * {start ns, end ns (%globaltimer, taken when thread 0 leaves the kernel),
  * kernel id, CTA index} to a device buffer of 262144 records shared by all
- * contexts of the process (records past its end are dropped).  Launches run one after another on the context's
- * stream, so sorting the records by start time and grouping consecutive
+ * contexts of the process (records past its end are dropped).  Launches run one
+ * after another on the context's stream (a paged kernel that starts early
+ * records from the end of its wait for the one before it), so sorting the records by start time and grouping consecutive
  * records of one kernel id recovers the launch sequence of a graph replay
  * with every launch's span and the gaps between launches.  In libdg.so both
  * calls return DG_ERR_UNSUPPORTED.
@@ -355,13 +356,14 @@ int64_t dg_debug_launch_count(const dg_ctx* ctx);
  * DG_K_EMBED_NORM 32, DG_K_RESIDUAL_NORM 33, DG_K_REDUCE_SPLITS 34,
  * DG_K_SWIGLU_SPLITS 35, DG_K_ROPE_QKV 36, DG_K_LMHEAD_MERGE_SAMPLE 37,
  * DG_K_ENTROPY_SAMPLE 38, DG_K_ROUTER_TOPK 39, DG_K_SAMPLE_ONLY 40,
- * DG_K_OTHER 50.
+ * DG_K_PAGED_PLAN 41, DG_K_PAGED_APPEND 42, DG_K_OTHER 50.
  * ------------------------------------------------------------------------- */
 enum {
   DG_K_GEMM_DENSE = 10, DG_K_GEMM_MOE = 11, DG_K_GEMM_LMHEAD = 13, DG_K_ATTENTION = 20, DG_K_ATTN_MERGE = 21,
   DG_K_ROUTE_DISPATCH = 30, DG_K_COMBINE_NORM = 31, DG_K_EMBED_NORM = 32, DG_K_RESIDUAL_NORM = 33,
   DG_K_REDUCE_SPLITS = 34, DG_K_SWIGLU_SPLITS = 35, DG_K_ROPE_QKV = 36, DG_K_LMHEAD_MERGE_SAMPLE = 37,
-  DG_K_ENTROPY_SAMPLE = 38, DG_K_ROUTER_TOPK = 39, DG_K_SAMPLE_ONLY = 40, DG_K_OTHER = 50
+  DG_K_ENTROPY_SAMPLE = 38, DG_K_ROUTER_TOPK = 39, DG_K_SAMPLE_ONLY = 40, DG_K_PAGED_PLAN = 41,
+  DG_K_PAGED_APPEND = 42, DG_K_OTHER = 50
 };
 
 typedef struct {
