@@ -13,6 +13,9 @@
 
 namespace {
 
+// the plan's CTAs: one per SM of a B200 (another number costs time, not the result)
+constexpr int kPlanCtas = 148;
+
 // log2 of a supported page size, -1 for any other
 int page_shift_of(int32_t page_size) {
   switch (page_size) {
@@ -252,9 +255,9 @@ dg_status dg_paged_plan(const dg_paged_plan_args* a, void* cuda_stream) {
   p.row_cap = a->row_capacity;
   // one CTA per request up to a wave of them; strips of a request's rows where
   // there are few requests of many rows
-  const int gx = std::min(a->batch, 148);
+  const int gx = std::min<int>(a->batch, kPlanCtas);
   const int64_t strips = cap / (B * 2 * PLAN_THREADS);
-  const int gy = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(strips, 148 / gx)));
+  const int gy = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(strips, kPlanCtas / gx)));
   return paged_launch(paged_plan_kernel, dim3(gx, gy), PLAN_THREADS, 0, cuda_stream, p);
 }
 

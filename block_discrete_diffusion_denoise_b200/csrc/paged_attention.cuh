@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(TOK_THREADS, 1) paged_token_kernel(const __gri
 // latency of its loads, of which each thread keeps several in flight; a small
 // tile's pieces are dealt out to groups of threads, joined in shared memory.
 // 2.8 us behind a token kernel, 5 us for the 16 tiles of a canvas over 2k keys
-// (26.6 MB of partial rows out of L2).
+// (26.7 MB of partial rows out of L2).
 // ----------------------------------------------------------------------------
 template <int ROWS>
 struct MergeCfg {
