@@ -43,7 +43,7 @@ __device__ __forceinline__ int64_t max64(int64_t a, int64_t b) { return a > b ? 
 //
 // Bound by latency (the ids and lengths of 200 requests are 0.2 MB): every CTA
 // sums the whole batch's lengths itself (two loads per 256 requests and thread)
-// instead of a second launch, then writes its own requests.  2.5 us for one
+// instead of a second launch, then writes its own requests.  2.6 us for one
 // request of 256 rows, 4.5 us for 200 requests of 25,000.
 // ----------------------------------------------------------------------------
 constexpr int PLAN_THREADS = 256;
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) paged_plan_kernel(const __grid_c
 // Bound by HBM: 2 x (Hq + 2 Hkv) x D x 2 bytes a row.  A thread takes eight
 // pairs (two 16-byte loads) of APPEND_HEADS heads, so the eight (cos, sin) of a
 // chunk are loaded once for them and eight loads are in flight per thread.
-// 16,000 rows of 16/8 heads of 176: 56.0 us, 6.4 TB/s (0.99 of the copy peak);
+// 16,000 rows of 16/8 heads of 176: 56.2 us, 6.4 TB/s (0.99 of the copy peak);
 // 62 us with 256 threads, 63 with two heads a thread, 65 with eight.
 // ----------------------------------------------------------------------------
 constexpr int APPEND_THREADS = 128;

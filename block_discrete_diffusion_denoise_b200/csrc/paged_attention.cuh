@@ -420,7 +420,7 @@ __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4],
 // memory and go on, and a warp of its own joins them.
 // One token for 64 requests of 256..8190 keys, 16/8 heads of 176: 234 us with
 // the merge, 6.6 TB/s (1.0 of the copy peak); 33 requests of up to 1500 keys, 8/2
-// heads of 128: 13.2 us; one request of 2048 keys: 9.3 us, of which the two blocks
+// heads of 128: 13.4 us; one request of 2048 keys: 9.5 us, of which the two blocks
 // of a CTA are one.
 // ----------------------------------------------------------------------------
 constexpr int TOK_ROWS = 16;

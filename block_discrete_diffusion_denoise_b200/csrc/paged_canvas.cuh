@@ -14,9 +14,9 @@
 // which keys the producers found.  At D = 176 a unit's products take 1777
 // cycles (48.6 per k-step of S, where both operands come from shared memory and
 // Q is read again for each, 88.5 of P V) and a unit 2050 to 2100.  A canvas of
-// 256 rows over 33,024 keys, 16/8 heads of 176: 95 us with the merge, 1000
-// TFLOP/s (115 us once the power limit lowers the clock); eight canvases over
-// 1.5k..6.5k keys 112 us; one over 2304 keys 21.5 us.
+// 256 rows over 33,024 keys, 16/8 heads of 176: 96 us with the merge, 1000
+// TFLOP/s (117 us once the power limit lowers the clock); eight canvases over
+// 1.5k..6.5k keys 114 us; one over 2304 keys 21.8 us.
 #pragma once
 
 #include "paged_attention.cuh"
