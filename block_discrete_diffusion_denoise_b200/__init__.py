@@ -179,6 +179,12 @@ def _invalid(msg: str):
     raise DGError(DG_ERR_INVALID_ARG, msg)
 
 
+def _stream_handle(stream) -> int:
+    """The cudaStream_t as a number, of whatever ctypes takes for it: a number, a c_void_p, a torch.cuda.Stream, None."""
+    h = getattr(stream, "_as_parameter_", stream)
+    return int(getattr(h, "value", h) or 0)
+
+
 def _check_tensor(t, dtype, n: int, what: str, device_type: str = "cuda", exact: bool = False,
                   optional: bool = False):
     """The checks a bare pointer cannot carry through the C ABI: t is a
@@ -274,7 +280,7 @@ class Context:
     def __init__(self, cfg: dict, weights: dict, stream=None):
         self.lib = load_library()
         self._batch = None            # batch of the last successful prefill
-        self._stream = int(getattr(stream, "value", stream) or 0)
+        self._stream = _stream_handle(stream)
         check_weights(cfg, weights, self._device_type)
         self._weights = weights
         c = dg_config()

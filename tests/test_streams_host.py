@@ -1,6 +1,8 @@
 """The order of torch's streams and a context's, without a device: what
 generate_blocks makes on torch's current stream is waited for before the
 context's next call, and its memory is kept until the context is done with it."""
+import ctypes
+
 import pytest
 import torch
 
@@ -92,3 +94,26 @@ def test_the_contexts_stream_waits_for_the_current_one_and_keeps_the_memory(hand
     current.cuda_stream = handle
     ctx._behind_torch(t)
     assert mine.waited == [current] and t.kept == [mine]
+
+
+class TorchStream:
+    _as_parameter_ = ctypes.c_void_p(88)      # what torch.cuda.Stream offers to ctypes
+
+
+@pytest.mark.parametrize("stream,handle", [(None, 0), (0, 0), (77, 77), (ctypes.c_void_p(78), 78),
+                                           (ctypes.c_void_p(None), 0), (TorchStream(), 88)])
+def test_a_context_knows_its_stream_in_every_form_that_it_takes(stream, handle, monkeypatch):
+    given = []
+
+    class Lib:
+        def dg_create(self, cfg, weights, stream, out):
+            given.append(stream)
+            return 7
+    monkeypatch.setattr(dg, "load_library", Lib)
+    monkeypatch.setattr(dg, "check_weights", lambda *a: None)
+    cfg = {n: 1 for n, _ in dg.dg_config._fields_}
+    weights = dict(embed=_i32(1), final_norm=_i32(1), layers=[{f: _i32(1) for f in dg.LAYER_FIELDS}])
+    ctx = dg.Context.__new__(dg.Context)
+    with pytest.raises(dg.DGError):
+        ctx.__init__(cfg, weights, stream=stream)
+    assert ctx._stream == handle and given == [stream]
